@@ -13,8 +13,10 @@
  * Scales come from max-calibration of the tensor in hand (the blog's post-training
  * calibration step reduced to one tensor), or are given (static scales, qattn_quantize_qkv).
  * The block's linear layers around the attention (the blog quantizes them with the same
- * schemes) are here too: qattn_gemm_fp8 / qattn_gemm_fp8_e4m3 (per-tensor FP8) and
- * qattn_gemm_fp4 (per-block FP4).
+ * schemes) are here too: qattn_gemm_fp8 / qattn_gemm_fp8_e4m3 (per-tensor FP8),
+ * qattn_gemm_fp4 (per-block FP4) and qattn_linear_int8 (8-bit integers, a scale for each token and
+ * output channel); and what lies between the QKV projection and the attention: the rotary table
+ * (qattn_rope_table) and the per-head norm with the rotation (qattn_norm_rope).
  *
  * Conventions for every entry point:
  *   - Pointers named *_dev or tensor data are DEVICE pointers on the current CUDA device; the
@@ -29,7 +31,7 @@
  *     found on the device (non-finite input, a timed-out wait, and in the checked build an
  *     index outside its buffer) are recorded in the device error word and reported by
  *     qattn_get_error().
- *   - Tensors are contiguous.  bf16 inputs are 16-byte aligned; E4M3 code buffers are 16-byte
+ *   - Tensors are contiguous unless the call takes strides.  bf16 inputs are 16-byte aligned; E4M3 code buffers are 16-byte
  *     aligned (the attention kernel reads them with TMA).
  *   - Only sm_100 devices are supported (QATTN_ERR_UNSUPPORTED otherwise).
  */
@@ -229,6 +231,106 @@ QATTN_API qattn_status qattn_gemm_fp4(const uint8_t* x_e2m1, const uint8_t* x_bs
                                       const float* sg_x_dev, const uint8_t* w_e2m1,
                                       const uint8_t* w_bscale, const float* sg_w_dev, void* y_bf16,
                                       int M, int N, int K, qattn_stream_t stream);
+
+/* 16-bit type of the activations of the calls below. */
+typedef enum {
+  QATTN_DTYPE_BF16 = 0,
+  QATTN_DTYPE_FP16 = 1
+} qattn_dtype;
+
+/* Type of the token positions of qattn_rope_table. */
+typedef enum {
+  QATTN_POS_INT32 = 0,
+  QATTN_POS_FLOAT32 = 1
+} qattn_pos_type;
+
+#define QATTN_ROPE_MAX_AXES 8      /* axes of a position */
+#define QATTN_ROPE_MAX_DIM 256     /* channels of a head; rotated channels */
+#define QATTN_NORM_ROPE_MAX_IO 12  /* tensors of one qattn_norm_rope call */
+#define QATTN_INT8_MAX_K 131071    /* K * 2^14 fits int32 */
+
+/* Rotary table of tokens with several position axes (stream or frame, row, column): the token
+ * positions that the transformer's Q and K rotation needs, made once for a resolution and kept.
+ *   pair i of axis a:  angle = pos[t, a] * theta[a]^(-2 i / axis_dims[a]),  i < axis_dims[a] / 2
+ *   table[t, p] = (cos angle, sin angle) in FP32, p counting the pairs of axis 0 first, then axis 1 ...
+ * pos_dev: device [tokens, n_axes] of pos_type, pos_stride elements (>= n_axes) between tokens;
+ * fractional and negative positions are allowed.  The angle is formed and reduced in 64 bits.
+ * axis_dims (even) and theta (> 0): HOST arrays of n_axes, read during the call.  table_dev: device
+ * [tokens, R / 2, 2] floats with R = sum of axis_dims <= QATTN_ROPE_MAX_DIM, 16-byte aligned.
+ * A non-finite position gives NaN entries for its axis. */
+QATTN_API qattn_status qattn_rope_table(const void* pos_dev, qattn_pos_type pos_type, int64_t pos_stride,
+                                        int tokens, int n_axes, const int* axis_dims,
+                                        const double* theta, float* table_dev, qattn_stream_t stream);
+
+/* One tensor of qattn_norm_rope (device pointers; strides in elements, all multiples of 8, the D
+ * channels of a head contiguous). */
+typedef struct {
+  const void* x;          /* [B, L, H, D] bf16 or FP16, 16-byte aligned: e.g. a slice of a QKV projection */
+  void* out;              /* [B, H, L, D]: same type, 16-byte aligned; or E4M3 codes, 8-byte aligned */
+  const float* weight;    /* [D] norm weight, 16-byte aligned; NULL: no norm */
+  const float* table;     /* [L, R / 2, 2] of qattn_rope_table, 16-byte aligned; NULL: no rotation */
+  float* amax;            /* E4M3: the given amax (input); else NULL or a running amax (in and out) */
+  float* scale_out;       /* E4M3: receives fl32(amax / 448) (1 when amax is 0) */
+  int64_t x_stride_b, x_stride_t, x_stride_h;
+  int64_t out_stride_b, out_stride_h, out_stride_t;
+  int64_t table_stride_b; /* floats between the tables of batch rows (a multiple of 4); 0: one for all */
+  int H, L;
+  int out_e4m3;           /* != 0: out receives E4M3 codes */
+} qattn_norm_rope_io;
+
+/* RMS norm of queries and keys for each head, rotary rotation, layout change to the attention's
+ * [B, H, L, D] and optionally the per-tensor FP8 FakeQuantize, in one pass and one launch for up to
+ * QATTN_NORM_ROPE_MAX_IO tensors (Q, K and V of the text and image streams; io is a HOST array read
+ * during the call).  For every head row x of D channels
+ *   n = x * (1 / sqrt(mean x^2 + eps)) * weight                      (weight NULL: n = x)
+ *   y = n with channel pairs p < rotary_dim / 2 rotated by table[t, p]: (c n0 - s n1, s n0 + c n1),
+ *       the pair being channels (2p, 2p + 1) with interleaved != 0, else (p, p + rotary_dim / 2)
+ * in FP32, rounded once to the 16-bit type.  Channels from rotary_dim on are not rotated.
+ * A tensor with neither weight nor table is copied (V).  E4M3: the codes and scale are those of
+ * qattn_quantize_fp8 of that 16-bit output under the given amax.  Running amax: *amax =
+ * max(*amax, max |y|) (the caller clears it before the first call of a calibration; tensors that
+ * share an amax are joined).  D % 8 == 0, D <= QATTN_ROPE_MAX_DIM; rotary_dim <= D, a multiple of 16.
+ * Heads may differ between tensors (grouped heads); L and H >= 1.  out must not overlap any x.
+ * A non-finite element, or a row whose squares pass FP32, records QATTN_ERR_NONFINITE (its outputs
+ * are what the arithmetic gives: NaN codes for NaN, +-448 for infinities); so does a non-finite given
+ * amax, and that tensor's codes and scale are not written. */
+QATTN_API qattn_status qattn_norm_rope(const qattn_norm_rope_io* io, int n_io, int B, int D,
+                                       int rotary_dim, int interleaved, float eps, qattn_dtype dtype,
+                                       qattn_stream_t stream);
+
+/* Symmetric 8-bit integer quantize with a scale for each row (token of an activation, output channel of
+ * a weight):
+ *   scale[m] = fl32(amax_m / 127), amax_m = max_k |x[m, k]|   (1 for a row of zeros)
+ *   out[m, k] = rint(127 x[m, k] / amax_m), ties to even, of the exact quotient: -127 .. 127
+ * x: device [M, K] bf16 or FP16, ldx elements between rows (any alignment; 16-byte aligned rows are
+ * read faster).  out_int8: device [M, K] bytes, ldo between rows, 16-byte aligned, ldo % 16 == 0
+ * (what lies between K and ldo is left as it was).  scale_dev: device [M].  A row with a
+ * non-finite element gets scale NaN and codes 0 and records QATTN_ERR_NONFINITE; the other rows are
+ * not affected. */
+QATTN_API qattn_status qattn_quantize_int8_rows(const void* x, int64_t ldx, qattn_dtype dtype, int M,
+                                                int K, int8_t* out_int8, int64_t ldo, float* scale_dev,
+                                                qattn_stream_t stream);
+
+/* 8-bit integer GEMM with a scale for each token and output channel: Y = A B^T,
+ *   y[m, n] = 16-bit( fl32(sum_k a8[m, k] b8[n, k]) * s_a[m] * s_b[n] (+ bias[n]) )
+ * with the sum exact in int32 (a8, b8 any int8 values, -128 included) and the rest in FP32.  a8 [M, K],
+ * b8 [N, K]: device int8, lda / ldb bytes between rows (multiples of 16), 16-byte aligned.
+ * y: device [M, N] bf16 or FP16, ldy elements between rows (16-byte aligned rows are written faster).
+ * s_a_dev [M], s_b_dev [N], bias_dev [N] or NULL: device floats.  M, N, K >= 1 of any size,
+ * K <= QATTN_INT8_MAX_K.  M <= 128 streams the weights once with K cut over clusters of CTAs, larger M
+ * runs on pairs of SMs; every path gives the same result.  An FP16 result past its range is infinite. */
+QATTN_API qattn_status qattn_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb,
+                                       void* y, int64_t ldy, qattn_dtype dtype, int M, int N, int K,
+                                       const float* s_a_dev, const float* s_b_dev, const float* bias_dev,
+                                       qattn_stream_t stream);
+
+/* A linear layer on 16-bit activations: qattn_quantize_int8_rows of x into x8 and s_x_dev (caller-owned,
+ * left filled), then qattn_gemm_int8 with them, the GEMM starting while the quantize runs (it loads weights
+ * until the codes are there).  Same results and rules as the two calls. */
+QATTN_API qattn_status qattn_linear_int8(const void* x, int64_t ldx, qattn_dtype dtype, int M, int N, int K,
+                                         int8_t* x8, int64_t ldx8, float* s_x_dev, const int8_t* w8,
+                                         int64_t ldw, const float* s_w_dev, const float* bias_dev, void* y,
+                                         int64_t ldy, qattn_stream_t stream);
 
 /* qattn_calibrate_quantize_fp8 without a caller workspace (the blog has no counterpart: this is
  * a calling convention, not part of the method).  For callers that cannot supply a scratch

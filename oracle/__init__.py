@@ -353,3 +353,64 @@ def gemm_e4m3(a8, b8, s_a, s_b, rows=None):
     a = tab[a8] * float(s_a)
     b = tab[np.asarray(b8)] * float(s_b)
     return a @ b.T, np.abs(a) @ np.abs(b).T
+
+
+# --- rotary table, per-head norm with rotation, 8-bit integer linear layer (FP64 definitions) -----
+def rope_angles(positions, axis_dims, theta) -> np.ndarray:
+    """[tokens, sum(axis_dims) / 2] angles: pair i of axis a is pos[t, a] * theta[a]^(-2 i / dim_a)."""
+    pos = np.asarray(positions, dtype=np.float64)
+    cols = []
+    for a, d in enumerate(axis_dims):
+        for i in range(d // 2):
+            cols.append(pos[:, a] * float(theta[a]) ** (-2.0 * i / d))
+    return np.stack(cols, 1)
+
+
+def norm_rope(x, weight, table, eps: float, interleaved: bool):
+    """x [B, L, H, D] float64 -> (y [B, H, L, D], size): the norm (weight None: none) and the rotation
+    (table [L, R/2, 2] or [B, L, R/2, 2], None: none) of every head row, unrounded, and the sum of
+    the magnitudes of the terms each value is made of."""
+    x = np.asarray(x, dtype=np.float64)
+    B, L, H, D = x.shape
+    y = x.copy()
+    if weight is not None:
+        y = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    size = np.abs(y)
+    if table is not None:
+        t = np.asarray(table, np.float64)
+        t = np.broadcast_to(t, (B, L) + t.shape[-2:])
+        half = t.shape[-2]
+        out = y.copy()
+        for p in range(half):
+            i, j = (2 * p, 2 * p + 1) if interleaved else (p, p + half)
+            c, s = t[:, :, None, p, 0], t[:, :, None, p, 1]
+            out[..., i] = y[..., i] * c - y[..., j] * s
+            out[..., j] = y[..., i] * s + y[..., j] * c
+            size[..., i] = np.abs(y[..., i] * c) + np.abs(y[..., j] * s)
+            size[..., j] = np.abs(y[..., i] * s) + np.abs(y[..., j] * c)
+        y = out
+    return y.transpose(0, 2, 1, 3), size.transpose(0, 2, 1, 3)
+
+
+def quantize_int8_rows(x):
+    """(codes int8 [M, K], scale float32 [M]) of x [M, K] (values of a 16-bit type): scale =
+    fl32(amax / 127), 1 for a row of zeros; code = the quotient 127 x / amax to the nearest integer, ties to
+    even.  The quotient of two such values is a half integer exactly or further from one than
+    FP64 rounds, so np.rint of the FP64 quotient is the definition."""
+    x = np.asarray(x, dtype=np.float64)
+    amax = np.abs(x).max(1)
+    scale = np.where(amax == 0, np.float32(1.0), amax.astype(np.float32) / np.float32(127.0)).astype(np.float32)
+    codes = np.rint(127.0 * x / np.where(amax == 0, 1.0, amax)[:, None])
+    return codes.astype(np.int8), scale
+
+
+def gemm_int8(a8, b8, s_a, s_b, bias=None):
+    """(Y, size) in FP64 of exact integer sums: Y[m, n] = (sum_k a8 b8) s_a[m] s_b[n] + bias[n];
+    size = |(sum) s_a s_b| + |bias|, what FP32 rounding errors are relative to."""
+    acc = (np.asarray(a8).astype(np.float64) @ np.asarray(b8).astype(np.float64).T)   # exact below 2^53
+    y = acc * np.asarray(s_a, np.float64)[:, None] * np.asarray(s_b, np.float64)[None]
+    size = np.abs(y)
+    if bias is not None:
+        b = np.asarray(bias, np.float64)[None]
+        y, size = y + b, size + np.abs(b)
+    return y, size

@@ -18,11 +18,13 @@ from . import _lib
 from ._lib import (MODE_FP4, MODE_FP8, QattnError, calibrate_amax, calibrate_quantize_fp4_block,
                    calibrate_quantize_fp8, calibrate_quantize_qkv, forward, forward_varlen,
                    forward_workspace_bytes, get_error, new_workspace, quantize_fp4_block,
-                   quantize_fp8, quantize_qkv, gemm_fp4, gemm_fp8, gemm_fp8_e4m3)
+                   quantize_fp8, quantize_qkv, gemm_fp4, gemm_fp8, gemm_fp8_e4m3, gemm_int8,
+                   linear_int8, norm_rope, NormRopeSegment, quantize_int8_rows, rope_table)
 
 __all__ = ["QuantizedAttention", "calibrate_amax", "quantize_fp8", "quantize_fp4_block",
            "calibrate_quantize_fp8", "calibrate_quantize_fp4_block", "calibrate_quantize_qkv",
-           "quantize_qkv", "gemm_fp8", "gemm_fp8_e4m3", "gemm_fp4",
+           "quantize_qkv", "gemm_fp8", "gemm_fp8_e4m3", "gemm_fp4", "quantize_int8_rows", "gemm_int8",
+           "linear_int8", "Int8Linear", "rope_table", "norm_rope", "NormRopeSegment",
            "new_workspace", "forward", "forward_workspace_bytes",
            "forward_varlen", "get_error", "QattnError", "MODE_FP8", "MODE_FP4"]
 
@@ -108,3 +110,37 @@ class QuantizedAttention:
     def __call__(self, q, k, v, stream=None):
         self.quantize(q, k, v, stream)
         return self.attend(stream)
+
+
+class Int8Linear:
+    """A linear layer of the block in 8-bit integers: y = x W^T (+ bias), W [N, K] quantized once with
+    a scale for each output channel, x [M, K] in every call with a scale for each token.
+
+    Holds the weight codes and the buffers of the activation codes for up to ``max_tokens`` rows, so that
+    calls allocate nothing but their result (give ``out`` to avoid that too).  Calls on one object
+    must not overlap on the device; stream order is enough.
+    """
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, max_tokens: int = 8704):
+        N, K = weight.shape
+        dev = weight.device
+        ld = -(-K // 16) * 16                       # rows of codes start on 16 bytes
+        self.out_features, self.in_features, self.max_tokens = N, K, int(max_tokens)
+        self.w8 = torch.zeros(N, ld, dtype=torch.int8, device=dev)[:, :K]
+        self.s_w = torch.empty(N, dtype=torch.float32, device=dev)
+        quantize_int8_rows(weight, self.w8, self.s_w)
+        self.bias = None if bias is None else bias.to(torch.float32).contiguous()
+        self._x8 = torch.empty(self.max_tokens, ld, dtype=torch.int8, device=dev)[:, :K]
+        self._s_x = torch.empty(self.max_tokens, dtype=torch.float32, device=dev)
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        shape = x.shape
+        x = x.reshape(-1, shape[-1])
+        M = x.shape[0]
+        if M > self.max_tokens:
+            raise ValueError(f"{M} tokens, made for {self.max_tokens}")
+        if out is None:
+            out = torch.empty(*shape[:-1], self.out_features, dtype=x.dtype, device=x.device)
+        linear_int8(x, self._x8[:M], self._s_x[:M], self.w8, self.s_w, out.view(-1, self.out_features),
+                    self.bias, stream)
+        return out

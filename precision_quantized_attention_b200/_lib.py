@@ -26,15 +26,18 @@ EXPORTS = (
     "qattn_forward_varlen", "qattn_get_error", "qattn_calibrate_quantize_fp8",
     "qattn_calibrate_quantize_fp4_block", "qattn_calibrate_quantize_fp8_noalloc",
     "qattn_calibrate_quantize_qkv", "qattn_quantize_qkv", "qattn_forward_ws", "qattn_gemm_fp8",
-    "qattn_gemm_fp8_e4m3", "qattn_gemm_fp4",
+    "qattn_gemm_fp8_e4m3", "qattn_gemm_fp4", "qattn_rope_table", "qattn_norm_rope",
+    "qattn_quantize_int8_rows", "qattn_gemm_int8", "qattn_linear_int8",
     "qattn_status_str", "qattn_last_cuda_error",
     "qattn_forward_workspace_bytes",
     "qattn_debug_set_wait_timeout_ns", "qattn_debug_inject_missing_q", "qattn_debug_capture_p_row",
     "qattn_debug_attention_plan", "qattn_build_info", "qattn_debug_inject_oob",
     "qattn_debug_use_pair_kernel",
 )
-_RETURNS_STATUS = EXPORTS[:15]
+_RETURNS_STATUS = EXPORTS[:20]
 FUSED_WORKSPACE_BYTES = 256     # QATTN_FUSED_WORKSPACE_BYTES
+DTYPE_BF16, DTYPE_FP16 = 0, 1
+NORM_ROPE_MAX_IO = 12           # QATTN_NORM_ROPE_MAX_IO
 
 
 class QattnError(RuntimeError):
@@ -52,6 +55,14 @@ class QuantIO(ctypes.Structure):
                 ("amax_dev", ctypes.c_void_p), ("scale_dev", ctypes.c_void_p),
                 ("out_e2m1", ctypes.c_void_p), ("blk_scale_e4m3", ctypes.c_void_p),
                 ("gscale_dev", ctypes.c_void_p)]
+
+
+class NormRopeIO(ctypes.Structure):
+    """qattn_norm_rope_io: one tensor of norm_rope."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "out", "weight", "table", "amax", "scale_out")]
+                + [(n, ctypes.c_int64) for n in ("x_stride_b", "x_stride_t", "x_stride_h", "out_stride_b",
+                                                 "out_stride_h", "out_stride_t", "table_stride_b")]
+                + [(n, ctypes.c_int) for n in ("H", "L", "out_e4m3")])
 
 
 class _Scales(ctypes.Structure):
@@ -83,6 +94,12 @@ def load() -> ctypes.CDLL:
     lib.qattn_gemm_fp8.argtypes = [P, P, P, I, I, I, P, P, P]
     lib.qattn_gemm_fp8_e4m3.argtypes = [P, P, P, P, I, I, I, P, P, P, P, P]
     lib.qattn_gemm_fp4.argtypes = [P, P, P, P, P, P, P, I, I, I, P]
+    L64, D64 = ctypes.c_int64, ctypes.POINTER(ctypes.c_double)
+    lib.qattn_rope_table.argtypes = [P, I, L64, I, I, ctypes.POINTER(I), D64, P, P]
+    lib.qattn_norm_rope.argtypes = [ctypes.POINTER(NormRopeIO), I, I, I, I, I, F, I, P]
+    lib.qattn_quantize_int8_rows.argtypes = [P, L64, I, I, I, P, L64, P, P]
+    lib.qattn_gemm_int8.argtypes = [P, L64, P, L64, P, L64, I, I, I, I, P, P, P, P]
+    lib.qattn_linear_int8.argtypes = [P, L64, I, I, I, I, P, L64, P, P, L64, P, P, P, L64, P]
     lib.qattn_forward.argtypes = [P, P, P, P, I, I, I, I, ctypes.POINTER(_Scales), F, I, P]
     lib.qattn_forward_varlen.argtypes = [P, P, P, P, P, I, I, I, I, I, ctypes.POINTER(_Scales),
                                          F, I, P]
@@ -313,6 +330,188 @@ def gemm_fp4(x_e2m1, x_bscale, sg_x, w_e2m1, w_bscale, sg_w, y, stream=None):
                                  _dev(sg_x, torch.float32, "sg_x"), _dev(w_e2m1, torch.uint8, "w_e2m1"),
                                  _dev(w_bscale, torch.uint8, "w_bscale"), _dev(sg_w, torch.float32, "sg_w"),
                                  _dev(y, torch.bfloat16, "y"), M, N, K, _stream(stream)), "qattn_gemm_fp4")
+
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16}
+
+
+def _on_device(device, stream, **tensors):
+    """The tensors of one call lie on one CUDA device, and the launch goes to a stream of it: the
+    library launches on the current device."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, not on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+
+
+def _rows(t: torch.Tensor, shape, what: str, align: int = 0) -> int:
+    """Row stride (in elements) of a 2-D tensor whose rows are contiguous."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    ld = t.stride(0) if rows > 1 else max(cols, t.stride(0) if t.stride(0) >= cols else cols)
+    if ld < cols:
+        raise ValueError(f"{what}: rows overlap")
+    if align and ld % align:
+        if rows > 1:
+            raise ValueError(f"{what}: the row stride must be a multiple of {align}")
+        ld = -(-cols // align) * align            # one row: its stride is not used
+    return ld
+
+
+def _vector(t, n: int, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of {n} elements")
+    return t.data_ptr()
+
+
+def rope_table(positions: torch.Tensor, axis_dims, table: torch.Tensor, theta=10000.0, stream=None):
+    """Rotary table of tokens with several position axes.  positions: int32 or float32 [tokens, axes]
+    (rows may be strided); axis_dims: rotated channels of each axis (even); theta: one base or one
+    for each axis; table: float32 [tokens, sum(axis_dims) / 2, 2], receives (cos, sin)."""
+    dims = [int(d) for d in axis_dims]
+    if positions.dim() != 2 or positions.shape[1] != len(dims) or positions.dtype not in (torch.int32, torch.float32):
+        raise ValueError(f"positions must be int32 or float32 [tokens, {len(dims)}]")
+    bases = [float(b) for b in theta] if hasattr(theta, "__len__") else [float(theta)] * len(dims)
+    if len(bases) != len(dims):
+        raise ValueError("theta needs one value or one for each axis")
+    tokens = positions.shape[0]
+    stride = _rows(positions, positions.shape, "positions")
+    if tuple(table.shape) != (tokens, sum(dims) // 2, 2):
+        raise ValueError(f"table must be [{tokens}, {sum(dims) // 2}, 2]")
+    _on_device(positions.device, stream, table=table)
+    n = len(dims)
+    _check(load().qattn_rope_table(positions.data_ptr(), int(positions.dtype == torch.float32), stride, tokens, n,
+                                   (ctypes.c_int * n)(*dims), (ctypes.c_double * n)(*bases),
+                                   _dev(table, torch.float32, "table"), _stream(stream)), "qattn_rope_table")
+
+
+class NormRopeSegment:
+    """One tensor of a norm_rope call.  x: bf16 or fp16 [B, L, H, D], any strides with contiguous
+    channels (a slice of a QKV projection); out: [B, H, L, D] of x's type, or uint8 for E4M3 codes
+    (any strides with contiguous channels); weight: float32 [D] or None (no norm); table: float32
+    [L, R/2, 2] or [B, L, R/2, 2] of rope_table, or None (no rotation); amax, scale: one-element
+    float32 tensors: with codes the given amax and the scale written, without codes amax may be a
+    running maximum of |out|."""
+
+    __slots__ = ("x", "out", "weight", "table", "amax", "scale")
+
+    def __init__(self, x, out, weight=None, table=None, amax=None, scale=None):
+        self.x, self.out, self.weight, self.table, self.amax, self.scale = x, out, weight, table, amax, scale
+
+
+def norm_rope(segments, eps: float = 1e-6, interleaved: bool = True, stream=None):
+    """Per-head RMS norm, rotation and layout change of up to 12 tensors (NormRopeSegment) in one
+    launch: Q, K and V of one or several token streams.  interleaved: channel pairs (2i, 2i+1), else
+    (i, i + R/2)."""
+    n = len(segments)
+    if not 1 <= n <= NORM_ROPE_MAX_IO:
+        raise ValueError(f"norm_rope takes 1 to {NORM_ROPE_MAX_IO} tensors")
+    first = segments[0].x
+    if first.dim() != 4 or first.dtype not in _DTYPES:
+        raise ValueError("x must be bfloat16 or float16 [B, L, H, D]")
+    B, D, dtype, device = first.shape[0], first.shape[3], first.dtype, first.device
+    rotary = 0
+    io = (NormRopeIO * n)()
+    for i, s in enumerate(segments):
+        x, out, table, d = s.x, s.out, s.table, io[i]
+        _on_device(device, stream, x=x, out=out, weight=s.weight, table=table, amax=s.amax, scale=s.scale)
+        if x.dim() != 4 or x.shape[0] != B or x.shape[3] != D or x.dtype != dtype:
+            raise ValueError("the tensors of a call have the same type, batch and head size")
+        _, L, H, _ = x.shape
+        if tuple(out.shape) != (B, H, L, D):
+            raise ValueError(f"out must be {[B, H, L, D]}, got {list(out.shape)}")
+        if out.dtype not in (dtype, torch.uint8):
+            raise ValueError("out must have x's type, or uint8 for E4M3 codes")
+        xs, os_ = x.stride(), out.stride()
+        if xs[3] != 1 or os_[3] != 1:
+            raise ValueError("the channels of a head must be contiguous")
+        # the stride of an axis of length 1 is not used
+        d.x_stride_b, d.x_stride_t, d.x_stride_h = (xs[0] if B > 1 else 0), (xs[1] if L > 1 else 0), (xs[2] if H > 1 else 0)
+        d.out_stride_b, d.out_stride_h, d.out_stride_t = (os_[0] if B > 1 else 0), (os_[1] if H > 1 else 0), (os_[2] if L > 1 else 0)
+        d.x, d.out, d.H, d.L, d.out_e4m3 = x.data_ptr(), out.data_ptr(), H, L, int(out.dtype == torch.uint8)
+        if d.out_e4m3 and (s.amax is None or s.scale is None):
+            raise ValueError("E4M3 codes need amax and scale")
+        d.weight = _vector(s.weight, D, "weight")
+        d.amax, d.scale_out = _vector(s.amax, 1, "amax"), _vector(s.scale, 1, "scale")
+        if table is not None:
+            ts = table.stride()
+            r = 2 * table.shape[-2] if table.dim() >= 3 else 0
+            if table.dtype != torch.float32 or table.dim() not in (3, 4) or table.shape[-1] != 2 or \
+                    table.shape[-3] != L or (table.dim() == 4 and table.shape[0] != B):
+                raise ValueError(f"table must be float32 [{L}, R/2, 2] or [{B}, {L}, R/2, 2]")
+            if ts[-1] != 1 or (r > 2 and ts[-2] != 2) or (L > 1 and ts[-3] != r):
+                raise ValueError("the rows of a table must be contiguous")
+            if rotary and r != rotary:
+                raise ValueError("the tables of a call have the same number of pairs")
+            rotary = r
+            d.table, d.table_stride_b = table.data_ptr(), (ts[0] if table.dim() == 4 and B > 1 else 0)
+    _check(load().qattn_norm_rope(io, n, B, D, rotary, int(bool(interleaved)), float(eps), _DTYPES[dtype],
+                                  _stream(stream)), "qattn_norm_rope")
+
+
+def _codes(t, what):
+    if t.dtype != torch.int8:
+        raise ValueError(f"{what} must be int8, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _act(t, what):
+    if t.dtype not in _DTYPES or t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D bfloat16 or float16 tensor")
+    return _DTYPES[t.dtype]
+
+
+def quantize_int8_rows(x, out, scale, stream=None):
+    """8-bit integer codes of x [M, K] (bf16 or fp16, rows may be strided) with a scale for each row:
+    out int8 [M, K] (row stride a multiple of 16), scale float32 [M] = amax / 127."""
+    dtype = _act(x, "x")
+    M, K = x.shape
+    ldx, ldo = _rows(x, (M, K), "x"), _rows(out, (M, K), "out", 16)
+    _on_device(x.device, stream, out=out, scale=scale)
+    _check(load().qattn_quantize_int8_rows(x.data_ptr(), ldx, dtype, M, K, _codes(out, "out"), ldo,
+                                           _vector(scale, M, "scale"), _stream(stream)), "qattn_quantize_int8_rows")
+
+
+def gemm_int8(a8, b8, y, s_a, s_b, bias=None, stream=None):
+    """y [M, N] (bf16 or fp16) = (a8 [M, K] b8 [N, K]^T) * s_a[m] * s_b[n] (+ bias[n]): int8 codes
+    (row strides multiples of 16), float32 scales and bias, exact int32 sums."""
+    dtype = _act(y, "y")
+    M, N = y.shape
+    if a8.dim() != 2:
+        raise ValueError("a8 must be [M, K]")
+    K = a8.shape[1]
+    lda, ldb, ldy = _rows(a8, (M, K), "a8", 16), _rows(b8, (N, K), "b8", 16), _rows(y, (M, N), "y")
+    _on_device(y.device, stream, a8=a8, b8=b8, s_a=s_a, s_b=s_b, bias=bias)
+    _check(load().qattn_gemm_int8(_codes(a8, "a8"), lda, _codes(b8, "b8"), ldb, y.data_ptr(), ldy, dtype, M, N, K,
+                                  _vector(s_a, M, "s_a"), _vector(s_b, N, "s_b"), _vector(bias, N, "bias"),
+                                  _stream(stream)), "qattn_gemm_int8")
+
+
+def linear_int8(x, x8, s_x, w8, s_w, y, bias=None, stream=None):
+    """quantize_int8_rows(x, x8, s_x) and gemm_int8(x8, w8, y, s_x, s_w, bias) in one call, the second
+    launch starting while the first runs."""
+    dtype = _act(x, "x")
+    M, K = x.shape
+    N = w8.shape[0]
+    if y.dtype != x.dtype:
+        raise ValueError("y must have x's type")
+    ldx, ld8 = _rows(x, (M, K), "x"), _rows(x8, (M, K), "x8", 16)
+    ldw, ldy = _rows(w8, (N, K), "w8", 16), _rows(y, (M, N), "y")
+    _on_device(x.device, stream, x8=x8, s_x=s_x, w8=w8, s_w=s_w, y=y, bias=bias)
+    _check(load().qattn_linear_int8(x.data_ptr(), ldx, dtype, M, N, K, _codes(x8, "x8"), ld8, _vector(s_x, M, "s_x"),
+                                    _codes(w8, "w8"), ldw, _vector(s_w, N, "s_w"), _vector(bias, N, "bias"),
+                                    y.data_ptr(), ldy, _stream(stream)), "qattn_linear_int8")
 
 
 def _scales(s_q, s_k, s_v):

@@ -64,6 +64,59 @@ cudaError_t launch_gemm_fp4(const uint8_t* x, const uint8_t* sx, const float* sg
                             const uint8_t* sw, const float* sg_w, void* y, int M, int N, int K,
                             int* err, uint64_t timeout_ns, int num_sms, cudaStream_t stream);
 
+// Rotary frequencies of the pairs of a table, in turns per unit of position, and their axes.
+struct RopeFreqs {
+  double turns[128];
+  uint8_t axis[128];
+};
+cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_stride, int tokens,
+                              int pairs, const RopeFreqs& f, float* table, int num_sms,
+                              cudaStream_t stream);
+
+// One tensor of a norm + rotation launch (rope.cu); strides in elements, channels contiguous.
+struct NormRopeSeg {
+  const void* x;
+  void* out;
+  const float* weight;         // [D], or null: no norm
+  const float* table;          // (cos, sin) pairs, or null: no rotation
+  float* amax;                 // E4M3: given amax; 16-bit: running amax or null
+  float* scale_out;            // E4M3: receives amax / 448
+  int64_t x_b, x_t, x_h, o_b, o_h, o_t, table_b;
+  int64_t items;               // warps of work (set by plan_norm_rope, as the next three)
+  int H, L, e4m3, chunks, steps;
+  unsigned first_block;
+};
+constexpr int kNormRopeMost = 12;
+struct NormRopeArgs {
+  NormRopeSeg seg[kNormRopeMost];
+  int n, D, R;
+  float eps, inv_d;
+  int* err;
+};
+bool plan_norm_rope(NormRopeArgs& a, int B, int num_sms, unsigned* grid);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, unsigned grid, int pairs, int fp16, cudaStream_t stream);
+
+// 8-bit integer linear layers (gemm_int8.cu): per-row quantize of 16-bit X [M, K], and
+// Y [M, N] = (A8 [M, K] B8 [N, K]^T) * s_a[m] * s_b[n] (+ bias[n]); ld*: row strides in elements.
+// The quantize lets the next launch of its stream start early; early = true (GEMM) makes use of it:
+// the preceding launch of the stream must then be that quantize.
+cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, int K, int8_t* out,
+                                   int64_t ldo, float* scale, int* err, cudaStream_t stream);
+struct GemmInt8Args {
+  int M, N, K;
+  int split;                   // set by the launcher: CTAs that share a tile's K range
+  int64_t ldy;
+  const float* s_a;
+  const float* s_b;
+  const float* bias;           // or null
+  void* y;
+  int* err;
+  uint64_t timeout_ns;
+};
+cudaError_t launch_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb,
+                             const GemmInt8Args& a, int fp16, int num_sms, bool early,
+                             cudaStream_t stream);
+
 // The attention with P left unquantized (QATTN_FLAG_P_UNQUANTIZED, a debug path; attn_debug.cu):
 // dense (cu_seqlens == nullptr: B, H, L) or varlen (cu_seqlens, nseq, max_seqlen, total_tokens, H).
 cudaError_t launch_attention_p_unquantized(const uint8_t* q8, const uint8_t* k8, const uint8_t* v8,

@@ -1,5 +1,6 @@
 // qattn_api.cu -- the C ABI (include/qattn.h): argument checks, device checks, launches.
 #include <cuda_runtime.h>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -15,6 +16,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr int64_t kMaxRowStride = (int64_t{1} << 40) - 16;   // row stride of a TMA map, in bytes
 
 struct DeviceInfo {
   cudaError_t setup = cudaSuccess;   // error of the set-up below, if any
@@ -77,6 +79,31 @@ qattn_status check_attention_common(const uint8_t* q8, const uint8_t* k8, const 
   if (D != 64 && D != 128) return QATTN_ERR_UNSUPPORTED;
   const int base = static_cast<int>(mode) & ~static_cast<int>(QATTN_FLAG_P_UNQUANTIZED);
   if (base != QATTN_MODE_FP8 && base != QATTN_MODE_FP4) return QATTN_ERR_INVALID_ARG;
+  return QATTN_OK;
+}
+
+qattn_status check_quant_rows(const void* x, int64_t ldx, qattn_dtype dtype, int M, int K, const int8_t* out,
+                              int64_t ldo, const float* scale) {
+  if (!x || !out || !scale || M < 1 || K < 1 || ldx < K || ldo < K || ldo % 16 != 0) return QATTN_ERR_INVALID_ARG;
+  if (dtype != QATTN_DTYPE_BF16 && dtype != QATTN_DTYPE_FP16) return QATTN_ERR_INVALID_ARG;
+  if (!aligned(x, 2) || !aligned(out, 16) || !aligned(scale, 4)) return QATTN_ERR_INVALID_ARG;
+  if (ldo > kMaxRowStride || K > 0x7FF00000) return QATTN_ERR_UNSUPPORTED;
+  return QATTN_OK;
+}
+
+qattn_status check_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb, const void* y,
+                             int64_t ldy, qattn_dtype dtype, int M, int N, int K, const float* s_a,
+                             const float* s_b, const float* bias) {
+  if (!a8 || !b8 || !y || !s_a || !s_b || M < 1 || N < 1 || K < 1) return QATTN_ERR_INVALID_ARG;
+  if (lda < K || ldb < K || ldy < N || lda % 16 != 0 || ldb % 16 != 0) return QATTN_ERR_INVALID_ARG;
+  if (dtype != QATTN_DTYPE_BF16 && dtype != QATTN_DTYPE_FP16) return QATTN_ERR_INVALID_ARG;
+  if (!aligned(a8, 16) || !aligned(b8, 16) || !aligned(y, 2) || !aligned(s_a, 4) || !aligned(s_b, 4) ||
+      (bias && !aligned(bias, 4)))
+    return QATTN_ERR_INVALID_ARG;
+  // |sum| <= K * 2^14 has to fit int32; tile counts have to fit an int
+  if (K > QATTN_INT8_MAX_K || lda > kMaxRowStride || ldb > kMaxRowStride) return QATTN_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(M) / 256 + 1) * (static_cast<int64_t>(N) / 64 + 1) > (1 << 30))
+    return QATTN_ERR_UNSUPPORTED;
   return QATTN_OK;
 }
 
@@ -326,6 +353,138 @@ qattn_status qattn_forward_ws(const uint8_t* q8, const uint8_t* k8, const uint8_
                                            d->err, g_timeout_ns, g_dbg,
                                            workspace_dev, workspace_bytes, d->num_sms,
                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_rope_table(const void* pos_dev, qattn_pos_type pos_type, int64_t pos_stride,
+                              int tokens, int n_axes, const int* axis_dims, const double* theta,
+                              float* table_dev, qattn_stream_t stream) {
+  if (!pos_dev || !axis_dims || !theta || !table_dev || tokens < 1) return QATTN_ERR_INVALID_ARG;
+  if (pos_type != QATTN_POS_INT32 && pos_type != QATTN_POS_FLOAT32) return QATTN_ERR_INVALID_ARG;
+  if (n_axes < 1 || n_axes > QATTN_ROPE_MAX_AXES || pos_stride < n_axes) return QATTN_ERR_INVALID_ARG;
+  if (!aligned(pos_dev, 4) || !aligned(table_dev, 16)) return QATTN_ERR_INVALID_ARG;
+  qattn::RopeFreqs f;
+  int pairs = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    const int d = axis_dims[a];
+    if (d < 2 || d % 2 != 0 || d > QATTN_ROPE_MAX_DIM) return QATTN_ERR_INVALID_ARG;
+    if (!(theta[a] > 0.0) || !(theta[a] < 1e300)) return QATTN_ERR_INVALID_ARG;
+    if (pairs + d / 2 > QATTN_ROPE_MAX_DIM / 2) return QATTN_ERR_UNSUPPORTED;
+    for (int i = 0; i < d / 2; ++i, ++pairs) {
+      // turns per unit of position: theta^(-2 i / d) / (2 pi)
+      f.turns[pairs] = std::pow(theta[a], -2.0 * i / d) * 0.15915494309189533577;
+      f.axis[pairs] = static_cast<uint8_t>(a);
+    }
+  }
+  DeviceInfo* d = nullptr;
+  qattn_status st = device_info(&d);
+  if (st != QATTN_OK) return st;
+  return from_cuda(qattn::launch_rope_table(pos_dev, pos_type == QATTN_POS_FLOAT32, pos_stride, tokens,
+                                            pairs, f, table_dev, d->num_sms,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_norm_rope(const qattn_norm_rope_io* io, int n_io, int B, int D, int rotary_dim,
+                             int interleaved, float eps, qattn_dtype dtype, qattn_stream_t stream) {
+  if (!io || n_io < 1 || B < 1) return QATTN_ERR_INVALID_ARG;
+  if (n_io > QATTN_NORM_ROPE_MAX_IO) return QATTN_ERR_UNSUPPORTED;
+  if (dtype != QATTN_DTYPE_BF16 && dtype != QATTN_DTYPE_FP16) return QATTN_ERR_INVALID_ARG;
+  if (D < 8 || D % 8 != 0 || rotary_dim < 0 || rotary_dim > D || rotary_dim % 16 != 0)
+    return QATTN_ERR_INVALID_ARG;
+  if (D > QATTN_ROPE_MAX_DIM) return QATTN_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return QATTN_ERR_INVALID_ARG;
+  qattn::NormRopeArgs a;
+  for (int i = 0; i < n_io; ++i) {
+    const qattn_norm_rope_io& t = io[i];
+    qattn::NormRopeSeg& s = a.seg[i];
+    if (!t.x || !t.out || t.H < 1 || t.L < 1) return QATTN_ERR_INVALID_ARG;
+    if (!aligned(t.x, 16) || (t.weight && !aligned(t.weight, 16)) || (t.table && !aligned(t.table, 16)) ||
+        (t.amax && !aligned(t.amax, 4)))
+      return QATTN_ERR_INVALID_ARG;
+    if ((t.x_stride_b | t.x_stride_t | t.x_stride_h | t.out_stride_b | t.out_stride_h | t.out_stride_t) % 8 != 0)
+      return QATTN_ERR_INVALID_ARG;
+    if (t.table && (rotary_dim == 0 || t.table_stride_b % 4 != 0)) return QATTN_ERR_INVALID_ARG;
+    // rows of the output must not share elements
+    if ((B > 1 && t.out_stride_b == 0) || (t.H > 1 && t.out_stride_h == 0) || (t.L > 1 && t.out_stride_t == 0))
+      return QATTN_ERR_INVALID_ARG;
+    if (t.out_e4m3) {
+      if (!t.amax || !t.scale_out || !aligned(t.scale_out, 4) || !aligned(t.out, 8)) return QATTN_ERR_INVALID_ARG;
+    } else if (!aligned(t.out, 16)) {
+      return QATTN_ERR_INVALID_ARG;
+    }
+    s.x = t.x;
+    s.out = t.out;
+    s.weight = t.weight;
+    s.table = t.table;
+    s.amax = t.amax;
+    s.scale_out = t.out_e4m3 ? t.scale_out : nullptr;
+    s.x_b = t.x_stride_b;
+    s.x_t = t.x_stride_t;
+    s.x_h = t.x_stride_h;
+    s.o_b = t.out_stride_b;
+    s.o_h = t.out_stride_h;
+    s.o_t = t.out_stride_t;
+    s.table_b = t.table_stride_b;
+    s.H = t.H;
+    s.L = t.L;
+    s.e4m3 = t.out_e4m3 != 0;
+  }
+  a.n = n_io;
+  a.D = D;
+  a.R = rotary_dim;
+  a.eps = eps;
+  a.inv_d = 1.0f / static_cast<float>(D);
+  DeviceInfo* d = nullptr;
+  qattn_status st = device_info(&d);
+  if (st != QATTN_OK) return st;
+  a.err = d->err;
+  unsigned grid = 0;
+  if (!qattn::plan_norm_rope(a, B, d->num_sms, &grid)) return QATTN_ERR_UNSUPPORTED;
+  return from_cuda(qattn::launch_norm_rope(a, grid, interleaved != 0, dtype == QATTN_DTYPE_FP16,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_quantize_int8_rows(const void* x, int64_t ldx, qattn_dtype dtype, int M, int K,
+                                      int8_t* out_int8, int64_t ldo, float* scale_dev,
+                                      qattn_stream_t stream) {
+  const qattn_status ck = check_quant_rows(x, ldx, dtype, M, K, out_int8, ldo, scale_dev);
+  if (ck != QATTN_OK) return ck;
+  DeviceInfo* d = nullptr;
+  qattn_status st = device_info(&d);
+  if (st != QATTN_OK) return st;
+  return from_cuda(qattn::launch_quant_int8_rows(x, ldx, dtype == QATTN_DTYPE_FP16, M, K, out_int8, ldo,
+                                                 scale_dev, d->err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb, void* y,
+                             int64_t ldy, qattn_dtype dtype, int M, int N, int K, const float* s_a_dev,
+                             const float* s_b_dev, const float* bias_dev, qattn_stream_t stream) {
+  const qattn_status ck = check_gemm_int8(a8, lda, b8, ldb, y, ldy, dtype, M, N, K, s_a_dev, s_b_dev, bias_dev);
+  if (ck != QATTN_OK) return ck;
+  DeviceInfo* d = nullptr;
+  qattn_status st = device_info(&d);
+  if (st != QATTN_OK) return st;
+  const qattn::GemmInt8Args a{M, N, K, 1, ldy, s_a_dev, s_b_dev, bias_dev, y, d->err, g_timeout_ns};
+  return from_cuda(qattn::launch_gemm_int8(a8, lda, b8, ldb, a, dtype == QATTN_DTYPE_FP16, d->num_sms, false,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_linear_int8(const void* x, int64_t ldx, qattn_dtype dtype, int M, int N, int K,
+                               int8_t* x8, int64_t ldx8, float* s_x_dev, const int8_t* w8, int64_t ldw,
+                               const float* s_w_dev, const float* bias_dev, void* y, int64_t ldy,
+                               qattn_stream_t stream) {
+  qattn_status ck = check_quant_rows(x, ldx, dtype, M, K, x8, ldx8, s_x_dev);
+  if (ck == QATTN_OK)
+    ck = check_gemm_int8(x8, ldx8, w8, ldw, y, ldy, dtype, M, N, K, s_x_dev, s_w_dev, bias_dev);
+  if (ck != QATTN_OK) return ck;
+  DeviceInfo* d = nullptr;
+  qattn_status st = device_info(&d);
+  if (st != QATTN_OK) return st;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int fp16 = dtype == QATTN_DTYPE_FP16;
+  st = from_cuda(qattn::launch_quant_int8_rows(x, ldx, fp16, M, K, x8, ldx8, s_x_dev, d->err, cs));
+  if (st != QATTN_OK) return st;
+  const qattn::GemmInt8Args a{M, N, K, 1, ldy, s_x_dev, s_w_dev, bias_dev, y, d->err, g_timeout_ns};
+  return from_cuda(qattn::launch_gemm_int8(x8, ldx8, w8, ldw, a, fp16, d->num_sms, true, cs));
 }
 
 qattn_status qattn_forward(const uint8_t* q8, const uint8_t* k8, const uint8_t* v8,
