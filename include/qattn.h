@@ -317,8 +317,8 @@ QATTN_API qattn_status qattn_quantize_int8_rows(const void* x, int64_t ldx, qatt
  * b8 [N, K]: device int8, lda / ldb bytes between rows (multiples of 16), 16-byte aligned.
  * y: device [M, N] bf16 or FP16, ldy elements between rows (16-byte aligned rows are written faster).
  * s_a_dev [M], s_b_dev [N], bias_dev [N] or NULL: device floats.  M, N, K >= 1 of any size,
- * K <= QATTN_INT8_MAX_K.  M <= 128 streams the weights once with K cut over clusters of CTAs, larger M
- * runs on pairs of SMs; every path gives the same result.  An FP16 result past its range is infinite. */
+ * K <= QATTN_INT8_MAX_K.  Few tokens (M <= 64) stream the weights once with K cut over clusters of CTAs, more
+ * run on pairs of SMs; every path gives the same result.  An FP16 result past its range is infinite. */
 QATTN_API qattn_status qattn_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb,
                                        void* y, int64_t ldy, qattn_dtype dtype, int M, int N, int K,
                                        const float* s_a_dev, const float* s_b_dev, const float* bias_dev,

@@ -43,28 +43,32 @@ __device__ __forceinline__ float from16(uint32_t bits) {
 // A row with a non-finite element gets scale NaN and codes 0 (its outputs become NaN, the other
 // rows are unaffected) and records DEV_ERR_NONFINITE.
 // -------------------------------------------------------------------------------------------
-// c127 = 127 * p and amax = p * (the row's), p a power of two (see scale_pow2); r = RN(1 / amax).
-__device__ __forceinline__ uint32_t code_int8(float x, float c127, float amax, float r) {
-  const float q = div_rn_by(c127 * x, amax, r);
-  return static_cast<uint32_t>(__float_as_int(q + 12582912.0f)) & 0xFFu;
-}
-
 // Power of two that brings a row's maximum to where 127 x cannot overflow and the quotient's residual
 // stays normal (bf16 reaches 2^127 and 2^-133); scaling by it is exact wherever the code is not 0.
 __device__ __forceinline__ float scale_pow2(float amax) {
   return amax > 0x1p+100f ? 0x1p-60f : amax < 0x1p-60f ? 0x1p+80f : 1.0f;
 }
 
+// How a row's codes are formed: p a power of two (scale_pow2), c = (127 p, 127 p), and for the quotient by
+// p * amax its rounded reciprocal and its negative, packed.
+struct RowCode {
+  f32x2 c, r, na;
+};
+
+// Codes of eight elements, two to an instruction until they are packed.
 template <bool FP16>
-__device__ __forceinline__ uint2 codes8(const uint32_t (&w)[4], float c127, float amax, float r) {
-  uint32_t c[8];
+__device__ __forceinline__ uint2 codes8(const uint32_t (&w)[4], const RowCode& k) {
+  const f32x2 magic = pack_f32x2(12582912.0f, 12582912.0f);
+  uint32_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    c[2 * i] = code_int8(from16<FP16>(w[i] & 0xFFFFu), c127, amax, r);
-    c[2 * i + 1] = code_int8(from16<FP16>(w[i] >> 16), c127, amax, r);
+    const f32x2 x = FP16 ? pack_f32x2(from16<true>(w[i] & 0xFFFFu), from16<true>(w[i] >> 16))
+                         : pack_f32x2(bf16_lo(w[i]), bf16_hi(w[i]));
+    float lo, hi;
+    unpack_f32x2(add_f32x2(div_f32x2(mul_f32x2(x, k.c), k.r, k.na), magic), lo, hi);
+    h[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);   // low bytes
   }
-  return make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
-                    c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
+  return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
 
 // Eight elements of a row from `at` (a multiple of 8); those past K read as zero.
@@ -132,11 +136,12 @@ __global__ void __launch_bounds__(256) k_quant_int8_rows(const uint16_t* __restr
   const float p2 = scale_pow2(amax), c127 = 127.0f * p2;
   amax *= p2;
   const float r = __frcp_rn(amax);
+  const RowCode k{pack_f32x2(c127, c127), pack_f32x2(r, r), pack_f32x2(-amax, -amax)};
   int8_t* orow = out + static_cast<int64_t>(m) * ldo;
   auto put = [&](const uint4& u, int at) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     uint2 c = make_uint2(0u, 0u);
-    if (finite) c = codes8<FP16>(w, c127, amax, r);
+    if (finite) c = codes8<FP16>(w, k);
     if (at + 8 <= K) {
       *reinterpret_cast<uint2*>(orow + at) = c;
     } else {
@@ -176,36 +181,47 @@ cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, 
 }
 
 // -------------------------------------------------------------------------------------------
-// Few tokens (M <= 128): bound by streaming the weights once.  One CTA takes 128 weight rows (the
-// MMA's M = 128, the TMEM lanes) against all tokens (N = TOK, 16 to 128) over a range of K; the
+// Few tokens: bound by streaming the weights once.  One CTA takes 128 weight rows (the
+// MMA's M = 128, the TMEM lanes) against a tile of tokens (N = TOK, 16 to 256) over a range of K; the
 // CTAs of a cluster share the 128 rows and cut K, so that a narrow layer still keeps every SM
 // loading.  int32 partial sums meet through distributed shared memory: exact, so neither the cut nor
 // the order changes a result, and no workspace or atomics are needed.
 //   warp 0      TMA producer; the weights of the first stages are requested before the wait for the
 //               preceding grid (the quantize writes only the activations)
 //   warp 1      MMA issuer and TMEM owner
-//   warps 2-5   epilogue: lane = output channel, column = token
+//   warps 2-9   epilogue: lane = output channel, column = token; two warps for each TMEM lane quarter,
+//               each with every other group of eight tokens
+// The producer and the issuer are picked with elect.sync: under `lane == 0` the compiler moves every operand of a
+// copy or MMA through a vote, and a K block took 600 clocks instead of 370 whatever its size.
 // -------------------------------------------------------------------------------------------
 namespace few {
 constexpr int BN = 128;                  // weight rows per CTA
 constexpr int BK = 128;
-constexpr int THREADS = 192;
+constexpr int THREADS = 320;
 constexpr int TILE_W = BN * BK;
 template <int TOK>
 struct Smem {
   static constexpr int TILE_X = TOK * BK;
   static constexpr int STAGE = TILE_W + TILE_X;
-  static constexpr int STAGES = (104 * 1024) / STAGE;          // two CTAs fit an SM
+  static constexpr int STAGES = (TOK <= 128 ? 104 : 200) * 1024 / STAGE;   // up to 128 tokens: two CTAs an SM
   static constexpr int OFF_W = 0, OFF_X = STAGES * TILE_W;
   static constexpr int OFF_BAR = OFF_X + STAGES * TILE_X;
   static constexpr int NBARS = 2 * STAGES + 2;                 // full, empty, accumulator, drain
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBARS;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int ALLOC = OFF_ABORT + 4 + 1024;
-  static_assert(TOK * 128 * 4 <= STAGES * STAGE, "partial sums reuse the stages");
+  static constexpr int OFF_SA = (OFF_ABORT + 4 + 15) / 16 * 16;   // the tile's token scales
+  static constexpr int ALLOC = OFF_SA + 4 * TOK + 1024;
+  static constexpr int ROW = TOK + 4;                          // words of a channel's partial sums (no conflicts)
+  static_assert(ROW * 128 * 4 <= STAGES * STAGE, "partial sums reuse the stages");
   static_assert(TILE_X % 1024 == 0, "alignment");
 };
 }  // namespace few
+
+// s_a may come from the preceding grid, still running when this one starts: no load that the compiler may
+// move in front of the wait for it or that may be served from the read-only path.
+__device__ __forceinline__ float row_scale(const GemmInt8Args& a, int m) {
+  return *const_cast<const volatile float*>(a.s_a + m);
+}
 
 template <int TOK, bool FP16>
 __global__ void __launch_bounds__(few::THREADS, 2)
@@ -223,7 +239,10 @@ __global__ void __launch_bounds__(few::THREADS, 2)
   const int lane = threadIdx.x & 31;
   const int split = args.split;                           // CTAs of the cluster
   const int rank = static_cast<int>(cluster_ctarank());
-  const int n0 = static_cast<int>(blockIdx.x) / split * BN;
+  const int tiles_n = (args.N + BN - 1) / BN;
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int n0 = tile % tiles_n * BN, m0 = tile / tiles_n * TOK;
+  const int tokens = args.M - m0 < TOK ? args.M - m0 : TOK;
   const int kblocks = (args.K + BK - 1) / BK;
   const int kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / split);
   const int nkb = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / split) - kb0;   // >= 1
@@ -233,12 +252,21 @@ __global__ void __launch_bounds__(few::THREADS, 2)
   constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC = 2 * STAGES, B_DRAIN = B_ACC + 1;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + S::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OFF_TMEM);
+  float* s_tok = reinterpret_cast<float*>(base + S::OFF_SA);
+  const int pre = nkb < STAGES ? nkb : STAGES;
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) { mbar_init(BAR(B_FULL + i), 1); mbar_init(BAR(B_EMPTY + i), 1); }
     mbar_init(BAR(B_ACC), 1);
     mbar_init(BAR(B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
+    fence_proxy_async();
+    // the producer's first weights are on their way while TMEM is allocated and the CTA assembles
+    (void)QATTN_IN_BOUNDS(args.err, n0 < args.N && m0 < args.M && nkb >= 1 && kb0 + nkb <= kblocks);
+    for (int u = 0; u < pre; ++u) {
+      mbar_arrive_expect_tx(BAR(B_FULL + u), S::STAGE);
+      tma_load_2d(base_u32 + S::OFF_W + u * TILE_W, &tm_w, BAR(B_FULL + u), (kb0 + u) * BK, n0);
+    }
   }
   if (warp == 1) {
     tmem_alloc(base_u32 + S::OFF_TMEM, TMEM_COLS);
@@ -253,30 +281,24 @@ __global__ void __launch_bounds__(few::THREADS, 2)
   bool got = false;                                // epilogue threads: the accumulator is complete
   if (warp == 0) {
     // ======================= TMA producer =======================
-    if (lane == 0) {
-      (void)QATTN_IN_BOUNDS(args.err, n0 < args.N && nkb >= 1 && kb0 + nkb <= kblocks);
-      const int pre = nkb < STAGES ? nkb : STAGES;
-      for (int u = 0; u < pre; ++u) {
-        mbar_arrive_expect_tx(BAR(B_FULL + u), S::STAGE);
-        tma_load_2d(base_u32 + S::OFF_W + u * TILE_W, &tm_w, BAR(B_FULL + u), (kb0 + u) * BK, n0);
-      }
+    if (elect_one()) {
       grid_wait_prior();
       for (int u = 0; u < pre; ++u)
-        tma_load_2d(base_u32 + S::OFF_X + u * S::TILE_X, &tm_x, BAR(B_FULL + u), (kb0 + u) * BK, 0);
+        tma_load_2d(base_u32 + S::OFF_X + u * S::TILE_X, &tm_x, BAR(B_FULL + u), (kb0 + u) * BK, m0);
       int u = pre;
       for (; u < nkb; ++u) {
         const int s = u % STAGES;
         if (!mbar_wait(BAR(B_EMPTY + s), ((u / STAGES) - 1) & 1, tlim, abort_flag, args.err)) break;
         mbar_arrive_expect_tx(BAR(B_FULL + s), S::STAGE);
         tma_load_2d(base_u32 + S::OFF_W + s * TILE_W, &tm_w, BAR(B_FULL + s), (kb0 + u) * BK, n0);
-        tma_load_2d(base_u32 + S::OFF_X + s * S::TILE_X, &tm_x, BAR(B_FULL + s), (kb0 + u) * BK, 0);
+        tma_load_2d(base_u32 + S::OFF_X + s * S::TILE_X, &tm_x, BAR(B_FULL + s), (kb0 + u) * BK, m0);
       }
       for (int j = u - 1; j >= 0 && j >= u - STAGES; --j)
         mbar_drain(BAR(B_FULL + j % STAGES), (j / STAGES) & 1, tlim);
     }
   } else if (warp == 1) {
     // ======================= MMA issuer =======================
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t IDESC = idesc_s8_s32(BN, TOK);
       bool ok = true;
       for (int u = 0; u < nkb; ++u) {
@@ -296,59 +318,85 @@ __global__ void __launch_bounds__(few::THREADS, 2)
       mbar_drain(BAR(B_DRAIN), 0, tlim);
     }
   } else {
-    // ======================= accumulator =======================
+    // ======================= epilogue: lane = output channel, column = token =======================
+    const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane, n = n0 + r;
+    float s_n = 0.0f, b_n = 0.0f;
+    if (n < args.N) {
+      s_n = __ldg(args.s_b + n);
+      if (args.bias) b_n = __ldg(args.bias + n);
+    }
+    // The token scales may come from the preceding grid, still running when this one starts: no load
+    // in front of the wait for it.  They pass through shared memory; read for each column from
+    // global memory they cost 128 round trips in a row (20 us).
+    grid_wait_prior();
+    for (int i = static_cast<int>(threadIdx.x) - 64; i < TOK; i += 256)
+      s_tok[i] = i < tokens ? row_scale(args, m0 + i) : 0.0f;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
     got = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_ACC), 0, tlim, abort_flag, args.err));
-    grid_wait_prior();                             // s_a comes from the preceding grid
+    uint16_t* y = static_cast<uint16_t*>(args.y) + m0 * args.ldy + n;
+    // four tokens from column c on (their scales on 16 bytes)
+    auto put4 = [&](const int (&a)[4], int c) {
+      const float4 st = *reinterpret_cast<const float4*>(s_tok + c);
+      const float s4[4] = {st.x, st.y, st.z, st.w};
+      uint16_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = to16<FP16>(fmaf(static_cast<float>(a[e]) * s4[e], s_n, b_n));
+      if (n < args.N) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < tokens && QATTN_IN_BOUNDS(args.err, m0 + c + e < args.M)) y[(c + e) * args.ldy] = o[e];
+      }
+    };
+    int* part = reinterpret_cast<int*>(base) + r * S::ROW;      // the stages are free: every MMA has completed
     if (got) {
       tc_fence_after();
-      const int quarter = warp & 3, r = quarter * 32 + lane;
       const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int n = n0 + r;
-      float s_n = 0.0f, b_n = 0.0f;
-      if (split == 1 && n < args.N) {
-        s_n = __ldg(args.s_b + n);
-        if (args.bias) b_n = __ldg(args.bias + n);
-      }
 #pragma unroll 1
-      for (int c = 0; c < TOK; c += 16) {
-        if (c >= args.M) break;                    // uniform: columns past the last token
-        uint32_t v[2][8];
-        tmem_ld8(acc + c, v[0]);
-        tmem_ld8(acc + c + 8, v[1]);
+      for (int c = half * 8; c < tokens; c += 16) {
+        uint32_t v[8];
+        tmem_ld8(acc + c, v);
         tmem_wait_ld();
+        if (split > 1) {
+          *reinterpret_cast<uint4*>(part + c) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(part + c + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+        } else {
+          const int a0[4] = {static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3])};
+          const int a1[4] = {static_cast<int>(v[4]), static_cast<int>(v[5]), static_cast<int>(v[6]), static_cast<int>(v[7])};
+          put4(a0, c);
+          put4(a1, c + 4);
+        }
+      }
+    }
+    if (split > 1) {
+      tc_fence_before();
+      cluster_sync();                              // partial sums of every CTA are in shared memory
+      if (got) {
+        // groups of four tokens go round the cluster's CTAs; all peers' loads of a group are in flight
+        // together
+        for (int g = rank + half * split; 4 * g < tokens; g += 2 * split) {
+          const uint32_t at = smem_u32(part + 4 * g);
+          int4 v[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int a = static_cast<int>(v[e >> 3][e & 7]);
-          if (split > 1) {                         // the stages are free: every MMA has completed
-            *reinterpret_cast<int*>(base + ((c + e) * 128 + r) * 4) = a;
-          } else if (n < args.N && c + e < args.M) {
-            const float y = fmaf(static_cast<float>(a) * __ldg(args.s_a + c + e), s_n, b_n);
-            static_cast<uint16_t*>(args.y)[(c + e) * args.ldy + n] = to16<FP16>(y);
-          }
+          for (int p = 0; p < 8; ++p)
+            if (p < split) v[p] = ld_cluster_v4(mapa_shared(at, static_cast<uint32_t>(p)));
+          int a[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+          for (int p = 1; p < 8; ++p)
+            if (p < split) { a[0] += v[p].x; a[1] += v[p].y; a[2] += v[p].z; a[3] += v[p].w; }
+          put4(a, 4 * g);
         }
       }
     }
   }
 
-  tc_fence_before();
   if (split > 1) {
-    cluster_sync();                                // partial sums of every CTA are in shared memory
-    if (warp >= 2 && got) {
-      const int r = static_cast<int>(threadIdx.x) - 64, n = n0 + r;
-      if (n < args.N) {
-        const float s_n = __ldg(args.s_b + n), b_n = args.bias ? __ldg(args.bias + n) : 0.0f;
-        for (int m = rank; m < args.M; m += split) {       // tokens of this CTA
-          const uint32_t at = base_u32 + static_cast<uint32_t>((m * 128 + r) * 4);
-          int a = 0;
-          for (int p = 0; p < split; ++p) a += ld_cluster_s32(mapa_shared(at, static_cast<uint32_t>(p)));
-          const float y = fmaf(static_cast<float>(a) * __ldg(args.s_a + m), s_n, b_n);
-          if (QATTN_IN_BOUNDS(args.err, m < args.M && n < args.N))
-            static_cast<uint16_t*>(args.y)[m * args.ldy + n] = to16<FP16>(y);
-        }
-      }
+    if (warp < 2) {
+      tc_fence_before();
+      cluster_sync();                              // with the epilogue's first
     }
     cluster_sync();                                // the peers have read this CTA's sums
   } else {
+    tc_fence_before();
     __syncthreads();
   }
   if (warp == 1) {
@@ -363,13 +411,16 @@ __global__ void __launch_bounds__(few::THREADS, 2)
 //   warp 0 (both CTAs)  TMA producer of its 128 rows of A and BN / 2 rows of B, into a ring whose
 //                       `full` barriers live in the leading CTA
 //   warp 1              TMEM owner; in the leading CTA the MMA issuer (two accumulators)
-//   warps 2-5 (both)    epilogue of the CTA's 128 rows, overlapping the next tile's MMAs
+//   warps 2-9 (both)    epilogue of the CTA's 128 rows, overlapping the next tile's MMAs; two warps for
+//                       each TMEM lane quarter, each with half of the columns
+// (The producer and the issuer are picked with elect.sync, see above: 470 clocks a K block instead of 684.)
 // Tiles are visited m-fastest.  Every wait is bounded and both CTAs reach both cluster barriers.
 // -------------------------------------------------------------------------------------------
 namespace pair8 {
 constexpr int BM = 256;
 constexpr int BK = 128;
-constexpr int THREADS = 192;
+constexpr int THREADS = 320;
+constexpr int EPI_WARPS = 8;
 constexpr int TILE_A = (BM / 2) * BK;
 template <int BN>
 struct Smem {
@@ -380,7 +431,9 @@ struct Smem {
   static constexpr int NBARS = 2 * STAGES + 4 + 1;
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBARS;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int ALLOC = OFF_ABORT + 4 + 1024;
+  static constexpr int OFF_T = (OFF_ABORT + 4 + 15) / 16 * 16; // per epilogue warp: 32 x 32 16-bit outputs,
+  static constexpr int WARP_T = 32 * 64 + 2 * (BN / 2) * 4;     // and its columns' scales and biases
+  static constexpr int ALLOC = OFF_T + EPI_WARPS * WARP_T + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   static constexpr uint32_t STAGE_TX = 2u * (TILE_A + TILE_B);
   static_assert(TILE_B % 1024 == 0, "alignment");
@@ -388,45 +441,50 @@ struct Smem {
 };
 }  // namespace pair8
 
-// 32 columns of one output row: y = acc * s_a * s_b + bias, 16-byte stores where the row is
-// aligned and the chunk lies inside the output.
+// 32 x 32 outputs of a warp (lane = row m of the accumulator, columns n ..): y = acc * s_a * s_b + bias, through
+// shared memory so that a store instruction writes whole rows: 8 rows of 64 bytes where rows start on 16 bytes, else
+// one row's 32 neighbours.  Stored by the lanes as they hold the rows, an instruction touches 32 lines (the epilogue
+// then took twice the time, and at an odd N 4.5 times).  sb, bias: the 32 columns' values in shared memory.
 template <bool FP16>
-__device__ __forceinline__ void epilogue_int8(const GemmInt8Args& a, const uint32_t (&v)[32], float s_m,
-                                              int m, int n, bool vec) {
-  if (!QATTN_IN_BOUNDS(a.err, m < a.M && n < a.N)) return;
-  uint16_t* y = static_cast<uint16_t*>(a.y) + m * a.ldy + n;
-  if (vec && n + 32 <= a.N) {
+__device__ __forceinline__ void epilogue_int8(const GemmInt8Args& a, const uint32_t (&v)[32], float s_m, int m_warp,
+                                              int n, bool vec, const float* sb, const float* bias, uint8_t* tile) {
+  if (!QATTN_IN_BOUNDS(a.err, n < a.N)) return;
+  const int lane = threadIdx.x & 31;
+  const int rows = min(32, a.M - m_warp);          // may be <= 0
+  // 16-byte piece j of row r lies at piece j ^ (r / 2 % 4): no bank conflict either way
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint32_t p[4];
-      const float4* sp = reinterpret_cast<const float4*>(a.s_b + n + 8 * g);
-      const float4 s0 = __ldg(sp), s1 = __ldg(sp + 1);
-      float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
-      if (a.bias) {
-        const float4* bp = reinterpret_cast<const float4*>(a.bias + n + 8 * g);
-        b0 = __ldg(bp);
-        b1 = __ldg(bp + 1);
-      }
-      const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-      const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+  for (int j = 0; j < 4; ++j) {
+    const float4 s0 = *reinterpret_cast<const float4*>(sb + 8 * j), s1 = *reinterpret_cast<const float4*>(sb + 8 * j + 4);
+    const float4 b0 = *reinterpret_cast<const float4*>(bias + 8 * j), b1 = *reinterpret_cast<const float4*>(bias + 8 * j + 4);
+    const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+    uint32_t p[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 8 * g + 2 * e;
-        const float lo = fmaf(static_cast<float>(static_cast<int>(v[i])) * s_m, s[2 * e], b[2 * e]);
-        const float hi = fmaf(static_cast<float>(static_cast<int>(v[i + 1])) * s_m, s[2 * e + 1], b[2 * e + 1]);
-        p[e] = static_cast<uint32_t>(to16<FP16>(lo)) | (static_cast<uint32_t>(to16<FP16>(hi)) << 16);
-      }
-      reinterpret_cast<uint4*>(y)[g] = make_uint4(p[0], p[1], p[2], p[3]);
+    for (int e = 0; e < 4; ++e) {
+      const int i = 8 * j + 2 * e;
+      const float lo = fmaf(static_cast<float>(static_cast<int>(v[i])) * s_m, sv[2 * e], bv[2 * e]);
+      const float hi = fmaf(static_cast<float>(static_cast<int>(v[i + 1])) * s_m, sv[2 * e + 1], bv[2 * e + 1]);
+      p[e] = static_cast<uint32_t>(to16<FP16>(lo)) | (static_cast<uint32_t>(to16<FP16>(hi)) << 16);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      if (n + e < a.N) {
-        const float b = a.bias ? __ldg(a.bias + n + e) : 0.0f;
-        y[e] = to16<FP16>(fmaf(static_cast<float>(static_cast<int>(v[e])) * s_m, __ldg(a.s_b + n + e), b));
-      }
-    }
+    *reinterpret_cast<uint4*>(tile + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
   }
+  __syncwarp();
+  uint16_t* y = static_cast<uint16_t*>(a.y) + m_warp * a.ldy + n;
+  if (vec && n + 32 <= a.N) {
+    const int j = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      if (r < rows)
+        *reinterpret_cast<uint4*>(y + r * a.ldy + 8 * j) =
+            *reinterpret_cast<const uint4*>(tile + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+    }
+  } else if (n + lane < a.N) {
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+      y[r * a.ldy + lane] = *reinterpret_cast<const uint16_t*>(tile + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+  }
+  __syncwarp();
 }
 
 template <int BN, bool FP16>
@@ -458,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OFF_TMEM);
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) { mbar_init(BAR(B_FULL + i), 1); mbar_init(BAR(B_EMPTY + i), 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(BAR(B_ACCF + b), 1); mbar_init(BAR(B_ACCE + b), 8); }
+    for (int b = 0; b < 2; ++b) { mbar_init(BAR(B_ACCF + b), 1); mbar_init(BAR(B_ACCE + b), 2 * EPI_WARPS); }
     mbar_init(BAR(B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -475,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
 
   if (warp == 0) {
     // ======================= TMA producer (both CTAs) =======================
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&tm_a);
       tma_prefetch_desc(&tm_b);
       grid_wait_prior();
@@ -504,9 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
     }
   } else if (warp == 1) {
     // ======================= MMA issuer (leading CTA) =======================
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       constexpr uint32_t IDESC = idesc_s8_s32(BM, BN);
-      const uint32_t peer = rank ^ 1u;
       int u = 0, i = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += npairs, ++i) {
@@ -528,13 +585,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
           for (int kk = 0; kk < BK / 32; ++kk)
             mma_i8_ss_pair(acc, smem_desc(a_s + kk * 32, 16, 1024, 2u), smem_desc(b_s + kk * 32, 16, 1024, 2u),
                            IDESC, (kb > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_pair(BAR(B_EMPTY + s));                      // stage free in both CTAs
-          mma_commit_pair(mapa_shared(BAR(B_EMPTY + s), peer));
+          mma_commit_pair_both(BAR(B_EMPTY + s));                 // stage free in both CTAs
         }
-        if (ok) {
-          mma_commit_pair(BAR(B_ACCF + ab));                      // accumulator complete
-          mma_commit_pair(mapa_shared(BAR(B_ACCF + ab), peer));
-        }
+        if (ok) mma_commit_pair_both(BAR(B_ACCF + ab));           // accumulator complete
       }
       mma_commit_pair(BAR(B_DRAIN));
       mbar_drain(BAR(B_DRAIN), 0, tlim);
@@ -542,27 +595,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
   } else {
     // ======================= epilogue warps (both CTAs) =======================
     grid_wait_prior();                             // s_a comes from the preceding grid
-    const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;
+    constexpr int COLS = BN / 2;                   // of this warp
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const bool vec = ((reinterpret_cast<uintptr_t>(args.y) | reinterpret_cast<uintptr_t>(args.s_b) |
-                       reinterpret_cast<uintptr_t>(args.bias)) & 15) == 0 && args.ldy % 8 == 0;
+    uint8_t* stage = base + S::OFF_T + (warp - 2) * S::WARP_T;
+    float* sb = reinterpret_cast<float*>(stage + 32 * 64);
+    float* bias = sb + COLS;
+    const bool vec = (reinterpret_cast<uintptr_t>(args.y) & 15) == 0 && args.ldy % 8 == 0;
     int i = 0;
     for (int t = pair; t < tiles; t += npairs, ++i) {
       const int ab = i & 1;
+      const int m_warp = (t % tiles_m) * BM + static_cast<int>(rank) * (BM / 2) + quarter * 32, m = m_warp + lane;
+      const int n0 = (t / tiles_m) * BN + half * COLS;
+      const float s_m = m < args.M ? row_scale(args, m) : 0.0f;
+#pragma unroll
+      for (int e = lane; e < COLS; e += 32) {
+        sb[e] = n0 + e < args.N ? __ldg(args.s_b + n0 + e) : 0.0f;
+        bias[e] = args.bias && n0 + e < args.N ? __ldg(args.bias + n0 + e) : 0.0f;
+      }
+      __syncwarp();
       const bool ok = mbar_wait(BAR(B_ACCF + ab), (i >> 1) & 1, tlim, abort_flag, args.err);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
-      const int m = (t % tiles_m) * BM + static_cast<int>(rank) * (BM / 2) + r;
-      const int n0 = (t / tiles_m) * BN;
-      const float s_m = m < args.M ? __ldg(args.s_a + m) : 0.0f;
-      const uint32_t acc = tmem + lane_off + static_cast<uint32_t>(ab * BN);
+      const uint32_t acc = tmem + lane_off + static_cast<uint32_t>(ab * BN + half * COLS);
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < COLS; c += 32) {
+        if (n0 + c >= args.N) break;               // uniform
         uint32_t v[32];
-        tmem_ld32(acc + c * 32, v);
+        tmem_ld32(acc + c, v);
         tmem_wait_ld();
-        if (m < args.M && n0 + c * 32 < args.N) epilogue_int8<FP16>(args, v, s_m, m, n0 + c * 32, vec);
+        epilogue_int8<FP16>(args, v, s_m, m_warp, n0 + c, vec, sb + c, bias + c, stage);
       }
       tc_fence_before();
       __syncwarp();
@@ -627,13 +689,13 @@ static cudaError_t launch_ex(K kernel, DeviceOnce& once, dim3 grid, unsigned clu
   return cudaLaunchKernelEx(&cfg, kernel, a, b, args);
 }
 
-// How many CTAs share 128 weight rows: enough to give every SM a CTA, with at least four K blocks
-// each.
-static int few_split(int N, int K, int num_sms) {
-  const int tiles = (N + few::BN - 1) / few::BN, kblocks = (K + few::BK - 1) / few::BK;
-  int split = num_sms / tiles;
+// How many CTAs share 128 weight rows and a token tile: enough to give every SM a CTA, with at least four
+// K blocks each.
+static int few_split(int64_t tiles, int K, int num_sms) {
+  const int kblocks = (K + few::BK - 1) / few::BK;
+  int64_t split = num_sms / tiles;
   if (split > kblocks / 4) split = kblocks / 4;
-  return split < 1 ? 1 : split > 8 ? 8 : split;
+  return split < 1 ? 1 : split > 8 ? 8 : static_cast<int>(split);
 }
 
 template <int TOK, bool FP16>
@@ -643,11 +705,11 @@ static cudaError_t launch_few(const int8_t* x, int64_t ldx, const int8_t* w, int
   CUtensorMap mw, mx;
   if (!make_map_rows(&mw, w, a.N, a.K, ldw, few::BN) || !make_map_rows(&mx, x, a.M, a.K, ldx, TOK))
     return cudaErrorInvalidValue;
+  const int64_t tiles = (static_cast<int64_t>(a.N) + few::BN - 1) / few::BN * ((a.M + TOK - 1) / TOK);
   GemmInt8Args b = a;
-  b.split = few_split(a.N, a.K, num_sms);
-  const dim3 grid(static_cast<unsigned>((a.N + few::BN - 1) / few::BN * b.split));
-  return launch_ex(k_gemm_int8_few<TOK, FP16>, once, grid, static_cast<unsigned>(b.split), few::THREADS,
-                   few::Smem<TOK>::ALLOC, early, stream, mw, mx, b);
+  b.split = few_split(tiles, a.K, num_sms);
+  return launch_ex(k_gemm_int8_few<TOK, FP16>, once, dim3(static_cast<unsigned>(tiles * b.split)),
+                   static_cast<unsigned>(b.split), few::THREADS, few::Smem<TOK>::ALLOC, early, stream, mw, mx, b);
 }
 
 template <int BN, bool FP16>
@@ -677,13 +739,37 @@ static cudaError_t launch_pair(const int8_t* x, int64_t ldx, const int8_t* w, in
                    pair8::Smem<BN>::ALLOC, early, stream, ma, mb, a);
 }
 
+// Columns of a pair tile.  In us for a pair of SMs at 1.9 GHz: a K block of 128 takes 0.17, 0.19 and 0.26 for 64, 128
+// and 256 columns (the last bound by the MMA, the others by the copies), an epilogue that nothing overlaps 0.8,
+// 1.2 and 3.5; the pairs run waves of tiles.  Measured, 74 pairs, K = 4096 (64 / 128 / 256 columns): 200 x 4096
+// 11.0 / 12.1 / 16.7 us, 512 x 4096 16.5 / 12.5 / 17.0, 1024 x 4096 27.6 / 18.2 / 17.5, 2048 x 12288 128 / 256: 80.6 /
+// 70.6.
+static int pair_columns(int M, int N, int K, int pairs) {
+  const int cols[3] = {64, 128, 256};
+  const double block[3] = {0.17, 0.19, 0.26}, tail[3] = {0.8, 1.2, 3.5};
+  const double kblocks = (K + pair8::BK - 1) / pair8::BK;
+  int best = 256;
+  double least = 1e30;
+  for (int i = 2; i >= 0; --i) {
+    const int64_t tiles = (static_cast<int64_t>(M) + pair8::BM - 1) / pair8::BM * ((N + cols[i] - 1) / cols[i]);
+    const double t = static_cast<double>((tiles + pairs - 1) / pairs) * kblocks * block[i] + tail[i];
+    if (t < least) {
+      least = t;
+      best = cols[i];
+    }
+  }
+  return best;
+}
+
 template <bool FP16>
 static cudaError_t launch_any(const int8_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const GemmInt8Args& a,
                               int num_sms, bool early, cudaStream_t stream) {
   if (a.M <= 16) return launch_few<16, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
   if (a.M <= 32) return launch_few<32, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
   if (a.M <= 64) return launch_few<64, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
-  if (a.M <= 128) return launch_few<128, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+  const int cols = pair_columns(a.M, a.N, a.K, num_sms / 2);
+  if (cols == 64) return launch_pair<64, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+  if (cols == 128) return launch_pair<128, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
   return launch_pair<256, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
 }
 

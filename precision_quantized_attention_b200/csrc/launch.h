@@ -82,8 +82,9 @@ struct NormRopeSeg {
   float* amax;                 // E4M3: given amax; 16-bit: running amax or null
   float* scale_out;            // E4M3: receives amax / 448
   int64_t x_b, x_t, x_h, o_b, o_h, o_t, table_b;
-  int64_t items;               // warps of work (set by plan_norm_rope, as the next three)
-  int H, L, e4m3, chunks, steps;
+  int H, L, e4m3;
+  int chunks, steps;           // set by plan_norm_rope, as the next two
+  uint32_t items;              // warps of work
   unsigned first_block;
 };
 constexpr int kNormRopeMost = 12;

@@ -51,6 +51,38 @@ __device__ __forceinline__ void div2_rn_by(float x0, float x1, float s, float r,
   q1 = copysignf(b, x1);
 }
 
+// Packed FP32 pairs (two floats in a 64-bit register pair): one instruction for two elements, each
+// half rounded as the scalar operation.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack_f32x2(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack_f32x2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul_f32x2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add_f32x2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma_f32x2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// The quotients of div_rn_by without its sign of a zero: rr = (r, r), ns = (-s, -s).
+__device__ __forceinline__ f32x2 div_f32x2(f32x2 x, f32x2 rr, f32x2 ns) {
+  const f32x2 q = mul_f32x2(x, rr);
+  return fma_f32x2(fma_f32x2(q, ns, x), rr, q);
+}
+
 // -------------------------------------------------------------------------------------------
 // Per-tensor FP8: s = fl32(amax / 448), code = e4m3(fl32(x / s)); amax == 0 gives s = 1.
 // -------------------------------------------------------------------------------------------

@@ -49,6 +49,12 @@ __device__ __forceinline__ void fence_mbar_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// Orders this thread's shared-memory writes (barriers it has initialised) before its later
+// asynchronous copies.
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -122,10 +128,12 @@ __device__ __forceinline__ float2 ld_shared_f32x2(uint32_t addr) {
   return v;
 }
 
-// A 32-bit word of the shared memory of any CTA of the cluster (address from mapa_shared).
-__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+// 16 bytes of the shared memory of any CTA of the cluster (address from mapa_shared, after the cluster barrier
+// that completes them: the address is formed behind it, so the load cannot move in front).
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr) {
+  int4 v;
+  asm("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(cluster_addr));
   return v;
 }
 

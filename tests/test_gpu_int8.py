@@ -135,7 +135,7 @@ def test_gemm_shapes(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(4, 128, 16384), (100, 384, 8192), (24, 4096, 1920), (1, 20000, 512),
-                                   (1200, 2100, 700), (640, 5000, 320)])
+                                   (1200, 2100, 700), (640, 5000, 320), (1000, 4090, 4100)])
 def test_gemm_larger(M, N, K):
     ops = _operands(M, N, K, seed=K)
     _check(_gemm(*ops), *ops)
