@@ -255,9 +255,9 @@ typedef enum {
  *   table[t, p] = (cos angle, sin angle) in FP32, p counting the pairs of axis 0 first, then axis 1 ...
  * pos_dev: device [tokens, n_axes] of pos_type, pos_stride elements (>= n_axes) between tokens;
  * fractional and negative positions are allowed.  The angle is formed and reduced in 64 bits.
- * axis_dims (even) and theta (> 0): HOST arrays of n_axes, read during the call.  table_dev: device
+ * axis_dims (even) and theta (>= 1): HOST arrays of n_axes, read during the call.  table_dev: device
  * [tokens, R / 2, 2] floats with R = sum of axis_dims <= QATTN_ROPE_MAX_DIM, 16-byte aligned.
- * A non-finite position gives NaN entries for its axis. */
+ * A non-finite position, or one past 2^31, gives NaN entries for its axis. */
 QATTN_API qattn_status qattn_rope_table(const void* pos_dev, qattn_pos_type pos_type, int64_t pos_stride,
                                         int tokens, int n_axes, const int* axis_dims,
                                         const double* theta, float* table_dev, qattn_stream_t stream);
@@ -286,9 +286,9 @@ typedef struct {
  *   y = n with channel pairs p < rotary_dim / 2 rotated by table[t, p]: (c n0 - s n1, s n0 + c n1),
  *       the pair being channels (2p, 2p + 1) with interleaved != 0, else (p, p + rotary_dim / 2)
  * in FP32, rounded once to the 16-bit type.  Channels from rotary_dim on are not rotated.
- * A tensor with neither weight nor table is copied (V).  E4M3: the codes and scale are those of
- * qattn_quantize_fp8 of that 16-bit output under the given amax.  Running amax: *amax =
- * max(*amax, max |y|) (the caller clears it before the first call of a calibration; tensors that
+ * A tensor with neither weight nor table is copied (V).  E4M3: code = e4m3(y / s), s = fl32(amax / 448) of the
+ * given amax, from the FP32 y, rounded once (a copied tensor gets exactly the codes of qattn_quantize_fp8).
+ * Running amax: *amax = max(*amax, max |16-bit y|) (the caller clears it before the first call of a calibration; tensors that
  * share an amax are joined).  D % 8 == 0, D <= QATTN_ROPE_MAX_DIM; rotary_dim <= D, a multiple of 16.
  * Heads may differ between tensors (grouped heads); L and H >= 1.  out must not overlap any x.
  * A non-finite element, or a row whose squares pass FP32, records QATTN_ERR_NONFINITE (its outputs

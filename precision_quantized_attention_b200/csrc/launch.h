@@ -64,14 +64,16 @@ cudaError_t launch_gemm_fp4(const uint8_t* x, const uint8_t* sx, const float* sg
                             const uint8_t* sw, const float* sg_w, void* y, int M, int N, int K,
                             int* err, uint64_t timeout_ns, int num_sms, cudaStream_t stream);
 
-// Rotary frequencies of the pairs of a table, in turns per unit of position, and their axes.
-struct RopeFreqs {
-  double turns[128];
-  uint8_t axis[128];
+// Rotary frequencies of the pairs of a table (turns per unit of position, times 2^64) and their axes.
+struct alignas(16) RopePair {
+  uint64_t turns;
+  int axis;
 };
-cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_stride, int tokens,
-                              int pairs, const RopeFreqs& f, float* table, int num_sms,
-                              cudaStream_t stream);
+struct RopeFreqs {
+  RopePair pair[128];
+};
+cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_stride, int tokens, int axes,
+                              int pairs, const RopeFreqs& f, float* table, int num_sms, cudaStream_t stream);
 
 // One tensor of a norm + rotation launch (rope.cu); strides in elements, channels contiguous.
 struct NormRopeSeg {
@@ -83,8 +85,12 @@ struct NormRopeSeg {
   float* scale_out;            // E4M3: receives amax / 448
   int64_t x_b, x_t, x_h, o_b, o_h, o_t, table_b;
   int H, L, e4m3;
-  int chunks, steps;           // set by plan_norm_rope, as the next two
-  uint32_t items;              // warps of work
+  // set by plan_norm_rope: heads (and its logarithm) and tokens a warp holds at once, warps for the L
+  // tokens, steps of a warp, warps for the H heads, warps of work, first block
+  int heads, heads_log2, tokens;
+  uint32_t rows;
+  int steps, chunks;
+  uint32_t items;
   unsigned first_block;
 };
 constexpr int kNormRopeMost = 12;

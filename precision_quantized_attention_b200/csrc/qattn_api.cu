@@ -367,19 +367,20 @@ qattn_status qattn_rope_table(const void* pos_dev, qattn_pos_type pos_type, int6
   for (int a = 0; a < n_axes; ++a) {
     const int d = axis_dims[a];
     if (d < 2 || d % 2 != 0 || d > QATTN_ROPE_MAX_DIM) return QATTN_ERR_INVALID_ARG;
-    if (!(theta[a] > 0.0) || !(theta[a] < 1e300)) return QATTN_ERR_INVALID_ARG;
+    if (!(theta[a] >= 1.0) || !(theta[a] < 1e300)) return QATTN_ERR_INVALID_ARG;
     if (pairs + d / 2 > QATTN_ROPE_MAX_DIM / 2) return QATTN_ERR_UNSUPPORTED;
     for (int i = 0; i < d / 2; ++i, ++pairs) {
-      // turns per unit of position: theta^(-2 i / d) / (2 pi)
-      f.turns[pairs] = std::pow(theta[a], -2.0 * i / d) * 0.15915494309189533577;
-      f.axis[pairs] = static_cast<uint8_t>(a);
+      // turns per unit of position, theta^(-2 i / d) / (2 pi) <= 0.16, times 2^64
+      const long double turns = std::pow(static_cast<long double>(theta[a]), -2.0L * i / d) * 0.159154943091895335769L;
+      f.pair[pairs].turns = static_cast<uint64_t>(turns * 18446744073709551616.0L + 0.5L);
+      f.pair[pairs].axis = a;
     }
   }
   DeviceInfo* d = nullptr;
   qattn_status st = device_info(&d);
   if (st != QATTN_OK) return st;
   return from_cuda(qattn::launch_rope_table(pos_dev, pos_type == QATTN_POS_FLOAT32, pos_stride, tokens,
-                                            pairs, f, table_dev, d->num_sms,
+                                            n_axes, pairs, f, table_dev, d->num_sms,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 

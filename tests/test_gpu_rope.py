@@ -5,7 +5,8 @@ the 32-bit sine or cosine (2^-23), and the 64-bit product (2^-50 of the angle, t
 rounding included).  A normed and rotated value: the sum of D squares (a lane's 8, then at most 5 shuffles)
 halves to 7 u, mean and eps u, rsqrt 2 ulp = 4 u, coefficient, its product with r, the product and the sum
 4 u, and the FP32 weight and table are inputs: 16 u, 24 allowed, of the magnitudes of its terms; then half a
-step of the 16-bit type.  Codes are those of the 16-bit output, exactly."""
+step of the 16-bit type.  An E4M3 code lies between the codes of the ends of the FP32 value's bar (28 u: two
+roundings of 1 / scale and one of the product more); a copied tensor's codes are exact."""
 import numpy as np
 import pytest
 import torch
@@ -141,34 +142,44 @@ def _e4m3(y, amax):
     return torch.from_numpy(q).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), s
 
 
+def check_codes(codes, scale, x, weight, table, eps, inter):
+    """Codes [B, H, L, D] of a normed and rotated tensor: between those of the ends of the value's bar."""
+    host = lambda t: None if t is None else t.double().cpu().numpy()
+    want, size = oracle.norm_rope(host(x), host(weight), host(table), eps, inter)
+    value = lambda v: torch.from_numpy(np.clip(v / scale, -448.0, 448.0)).float().to(torch.float8_e4m3fn).float().numpy()
+    got = codes.cpu().view(torch.float8_e4m3fn).float().numpy()
+    assert (value(want - 28 * U * size) <= got).all() and (got <= value(want + 28 * U * size)).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("D,inter", [(128, True), (64, False)])
+@pytest.mark.parametrize("D,R,inter", [(128, 128, True), (64, 64, False), (96, 32, False), (256, 256, False)])
 @pytest.mark.parametrize("amax", [3.0, 0.0, 1e-38, 2e-2, 3e38])
-def test_codes_are_the_quantized_16_bit_output(D, inter, dtype, amax):
+def test_codes(D, R, inter, dtype, amax):
     """Also with an amax below the largest value (saturation), of zero, and so small or large that the
-    scale leaves the range of the fast quotient."""
+    scale leaves the range of the fast path.  The copied tensor's are the framework's own quantize."""
     B, L, H = 2, 45, 6
     g = torch.Generator().manual_seed(D)
     x = torch.randn(B, L, H, D, generator=g).to(dtype).cuda()
     w = (1 + 0.1 * torch.randn(D, generator=g)).cuda()
-    a = torch.rand(L, D // 2, generator=g) * 9
+    a = torch.rand(L, R // 2, generator=g) * 9
     table = torch.stack([a.cos(), a.sin()], -1).cuda()
-    y = [torch.empty(B, H, L, D, dtype=dtype, device="cuda") for _ in range(2)]
-    c = [torch.full((B, H, L + 1, D), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2)]
-    am, sc = torch.full((2,), amax, device="cuda"), torch.zeros(2, device="cuda")
-    qa.norm_rope([qa.NormRopeSegment(x, y[0], weight=w, table=table), qa.NormRopeSegment(x, y[1])], interleaved=inter)
+    c = [torch.full((B, H, L + 1, D), 0x55, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    am, sc = torch.full((3,), amax, device="cuda"), torch.zeros(3, device="cuda")
     qa.norm_rope([qa.NormRopeSegment(x, c[0][:, :, :L], weight=w, table=table, amax=am[:1], scale=sc[:1]),
-                  qa.NormRopeSegment(x, c[1][:, :, :L], amax=am[1:], scale=sc[1:])], interleaved=inter)
+                  qa.NormRopeSegment(x, c[1][:, :, :L], amax=am[1:2], scale=sc[1:2]),
+                  qa.NormRopeSegment(x, c[2][:, :, :L], table=table, amax=am[2:], scale=sc[2:])], interleaved=inter)
     assert qa.get_error() == 0
-    for i in range(2):
-        want, s = _e4m3(y[i], np.float32(amax))
+    want, s = _e4m3(x.transpose(1, 2).contiguous(), np.float32(amax))
+    for i in range(3):
         assert np.float32(sc[i].item()) == s
-        assert torch.equal(c[i][:, :, :L].cpu(), want)
         assert bool((c[i][:, :, L] == 0x55).all())
-        if dtype == torch.bfloat16:                  # and so by the framework's own quantize
-            code, scale = torch.empty_like(want, device="cuda"), torch.zeros(1, device="cuda")
-            qa.quantize_fp8(y[i].contiguous(), am[i:i + 1], code, scale)
-            assert torch.equal(code.cpu(), want)
+    assert torch.equal(c[1][:, :, :L].cpu(), want)
+    check_codes(c[0][:, :, :L], float(s), x, w, table, 1e-6, inter)
+    check_codes(c[2][:, :, :L], float(s), x, None, table, 1e-6, inter)
+    if dtype == torch.bfloat16:
+        code, scale = torch.empty_like(want, device="cuda"), torch.zeros(1, device="cuda")
+        qa.quantize_fp8(x.transpose(1, 2).contiguous(), am[:1], code, scale)
+        assert torch.equal(code.cpu(), want)
 
 
 def test_running_amax_joins_streams_and_calls():

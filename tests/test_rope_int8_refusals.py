@@ -24,7 +24,7 @@ def _with(names, ok, kw):
     ({"tokens": 0}, INVALID), ({"n": 0}, INVALID), ({"n": 9}, INVALID), ({"dims": (16, 55, 56)}, INVALID),
     ({"dims": (16, 0, 56)}, INVALID), ({"dims": (128, 128, 2)}, UNSUPPORTED), ({"dims": (258, 2, 2)}, INVALID),
     ({"theta": (1e4, 0.0, 1e4)}, INVALID), ({"theta": (1e4, float("nan"), 1e4)}, INVALID),
-    ({"theta": (float("inf"),) * 3}, INVALID)])
+    ({"theta": (float("inf"),) * 3}, INVALID), ({"theta": (1e4, 0.5, 1e4)}, INVALID)])
 def test_rope_table_abi(kw, status):
     names = ("pos", "type", "stride", "tokens", "n", "dims", "theta", "table")
     a = _with(names, (FAKE, 0, 3, 16, 3, (16, 56, 56), (1e4,) * 3, FAKE), kw)
