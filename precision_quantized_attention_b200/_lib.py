@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -96,7 +97,7 @@ def load() -> ctypes.CDLL:
     lib.qattn_gemm_fp4.argtypes = [P, P, P, P, P, P, P, I, I, I, P]
     L64, D64 = ctypes.c_int64, ctypes.POINTER(ctypes.c_double)
     lib.qattn_rope_table.argtypes = [P, I, L64, I, I, ctypes.POINTER(I), D64, P, P]
-    lib.qattn_norm_rope.argtypes = [ctypes.POINTER(NormRopeIO), I, I, I, I, I, F, I, P]
+    lib.qattn_norm_rope.argtypes = [P, I, I, I, I, I, F, I, P]   # io: NormRopeIO array or its bytes
     lib.qattn_quantize_int8_rows.argtypes = [P, L64, I, I, I, P, L64, P, P]
     lib.qattn_gemm_int8.argtypes = [P, L64, P, L64, P, L64, I, I, I, I, P, P, P, P]
     lib.qattn_linear_int8.argtypes = [P, L64, I, I, I, I, P, L64, P, P, L64, P, P, P, L64, P]
@@ -333,45 +334,55 @@ def gemm_fp4(x_e2m1, x_bscale, sg_x, w_e2m1, w_bscale, sg_w, y, stream=None):
 
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16}
+_F32, _I8 = torch.float32, torch.int8
 
 
-def _on_device(device, stream, **tensors):
-    """The tensors of one call lie on one CUDA device, and the launch goes to a stream of it: the
-    library launches on the current device."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    if device.type != "cuda":
+def _launch_stream(index: int, stream):
+    """The stream handle of a call whose tensors lie on CUDA device `index` (of get_device()): the
+    library launches on the current device, so that is where they and the stream have to be."""
+    if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, not on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    current = torch._C._cuda_getDevice()          # a tensor of the device exists: CUDA is initialised
+    if index != current:
+        raise ValueError(f"the tensors are on cuda:{index}, not on the current device cuda:{current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream.cuda_stream
 
 
-def _rows(t: torch.Tensor, shape, what: str, align: int = 0) -> int:
+def _same_device(index: int, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the call's first tensor on "
+                             + (f"cuda:{index}" if index >= 0 else "cpu"))
+
+
+def _rows(t: torch.Tensor, rows: int, cols: int, what: str, align: int = 1) -> int:
     """Row stride (in elements) of a 2-D tensor whose rows are contiguous."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must be {[rows, cols]}, got {list(t.shape)}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
-    ld = t.stride(0) if rows > 1 else max(cols, t.stride(0) if t.stride(0) >= cols else cols)
+    if rows < 2:                                  # one row: its stride is not used
+        return -(-cols // align) * align
     if ld < cols:
         raise ValueError(f"{what}: rows overlap")
-    if align and ld % align:
-        if rows > 1:
-            raise ValueError(f"{what}: the row stride must be a multiple of {align}")
-        ld = -(-cols // align) * align            # one row: its stride is not used
+    if ld % align:
+        raise ValueError(f"{what}: the row stride must be a multiple of {align}")
     return ld
 
 
-def _vector(t, n: int, what: str):
+def _vector(t, n: int, index: int, what: str):
+    """Address of a contiguous float32 vector of n elements on the call's device, or None."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype is not _F32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous float32 tensor of {n} elements")
+    if t.get_device() != index:
+        _same_device(index, **{what: t})
     return t.data_ptr()
 
 
@@ -379,21 +390,22 @@ def rope_table(positions: torch.Tensor, axis_dims, table: torch.Tensor, theta=10
     """Rotary table of tokens with several position axes.  positions: int32 or float32 [tokens, axes]
     (rows may be strided); axis_dims: rotated channels of each axis (even); theta: one base or one
     for each axis; table: float32 [tokens, sum(axis_dims) / 2, 2], receives (cos, sin)."""
-    dims = [int(d) for d in axis_dims]
-    if positions.dim() != 2 or positions.shape[1] != len(dims) or positions.dtype not in (torch.int32, torch.float32):
-        raise ValueError(f"positions must be int32 or float32 [tokens, {len(dims)}]")
-    bases = [float(b) for b in theta] if hasattr(theta, "__len__") else [float(theta)] * len(dims)
-    if len(bases) != len(dims):
+    n = len(axis_dims)
+    if positions.dim() != 2 or positions.shape[1] != n or positions.dtype not in (torch.int32, _F32):
+        raise ValueError(f"positions must be int32 or float32 [tokens, {n}]")
+    bases = theta if hasattr(theta, "__len__") else [theta] * n
+    if len(bases) != n:
         raise ValueError("theta needs one value or one for each axis")
-    tokens = positions.shape[0]
-    stride = _rows(positions, positions.shape, "positions")
-    if tuple(table.shape) != (tokens, sum(dims) // 2, 2):
-        raise ValueError(f"table must be [{tokens}, {sum(dims) // 2}, 2]")
-    _on_device(positions.device, stream, table=table)
-    n = len(dims)
-    _check(load().qattn_rope_table(positions.data_ptr(), int(positions.dtype == torch.float32), stride, tokens, n,
-                                   (ctypes.c_int * n)(*dims), (ctypes.c_double * n)(*bases),
-                                   _dev(table, torch.float32, "table"), _stream(stream)), "qattn_rope_table")
+    tokens, pairs = positions.shape[0], sum(axis_dims) // 2
+    stride = _rows(positions, tokens, n, "positions")
+    if table.shape != (tokens, pairs, 2) or table.dtype is not _F32 or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous float32 [{tokens}, {pairs}, 2]")
+    index = positions.get_device()
+    _same_device(index, table=table)
+    handle = _launch_stream(index, stream)
+    _check(load().qattn_rope_table(positions.data_ptr(), int(positions.dtype is _F32), stride, tokens, n,
+                                   (ctypes.c_int * n)(*axis_dims), (ctypes.c_double * n)(*bases),
+                                   table.data_ptr(), handle), "qattn_rope_table")
 
 
 class NormRopeSegment:
@@ -410,6 +422,11 @@ class NormRopeSegment:
         self.x, self.out, self.weight, self.table, self.amax, self.scale = x, out, weight, table, amax, scale
 
 
+# qattn_norm_rope_io as bytes: 6 addresses, 7 strides, H, L, out_e4m3, padding
+_NORM_ROPE_IO = struct.Struct("@6P7q3i4x")
+assert _NORM_ROPE_IO.size == ctypes.sizeof(NormRopeIO)
+
+
 def norm_rope(segments, eps: float = 1e-6, interleaved: bool = True, stream=None):
     """Per-head RMS norm, rotation and layout change of up to 12 tensors (NormRopeSegment) in one
     launch: Q, K and V of one or several token streams.  interleaved: channel pairs (2i, 2i+1), else
@@ -418,50 +435,74 @@ def norm_rope(segments, eps: float = 1e-6, interleaved: bool = True, stream=None
     if not 1 <= n <= NORM_ROPE_MAX_IO:
         raise ValueError(f"norm_rope takes 1 to {NORM_ROPE_MAX_IO} tensors")
     first = segments[0].x
-    if first.dim() != 4 or first.dtype not in _DTYPES:
+    dtype = first.dtype
+    if first.dim() != 4 or dtype not in _DTYPES:
         raise ValueError("x must be bfloat16 or float16 [B, L, H, D]")
-    B, D, dtype, device = first.shape[0], first.shape[3], first.dtype, first.device
+    B, _, _, D = first.shape
+    index = first.get_device()
+    handle = _launch_stream(index, stream)
     rotary = 0
-    io = (NormRopeIO * n)()
-    for i, s in enumerate(segments):
-        x, out, table, d = s.x, s.out, s.table, io[i]
-        _on_device(device, stream, x=x, out=out, weight=s.weight, table=table, amax=s.amax, scale=s.scale)
-        if x.dim() != 4 or x.shape[0] != B or x.shape[3] != D or x.dtype != dtype:
+    seen = None                                   # the table looked at last: Q and K share one
+    io = bytearray(n * _NORM_ROPE_IO.size)
+    at = 0
+    for s in segments:
+        x, out = s.x, s.out
+        shape = x.shape
+        if x.dtype is not dtype or len(shape) != 4 or shape[0] != B or shape[3] != D:
             raise ValueError("the tensors of a call have the same type, batch and head size")
-        _, L, H, _ = x.shape
-        if tuple(out.shape) != (B, H, L, D):
+        _, L, H, _ = shape
+        if out.shape != (B, H, L, D):
             raise ValueError(f"out must be {[B, H, L, D]}, got {list(out.shape)}")
-        if out.dtype not in (dtype, torch.uint8):
+        codes = out.dtype is not dtype
+        if codes and out.dtype is not torch.uint8:
             raise ValueError("out must have x's type, or uint8 for E4M3 codes")
-        xs, os_ = x.stride(), out.stride()
-        if xs[3] != 1 or os_[3] != 1:
+        if x.get_device() != index or out.get_device() != index:
+            _same_device(index, x=x, out=out)
+        xb, xt, xh, xc = x.stride()
+        ob, oh, ot, oc = out.stride()
+        if xc != 1 or oc != 1:
             raise ValueError("the channels of a head must be contiguous")
         # the stride of an axis of length 1 is not used
-        d.x_stride_b, d.x_stride_t, d.x_stride_h = (xs[0] if B > 1 else 0), (xs[1] if L > 1 else 0), (xs[2] if H > 1 else 0)
-        d.out_stride_b, d.out_stride_h, d.out_stride_t = (os_[0] if B > 1 else 0), (os_[1] if H > 1 else 0), (os_[2] if L > 1 else 0)
-        d.x, d.out, d.H, d.L, d.out_e4m3 = x.data_ptr(), out.data_ptr(), H, L, int(out.dtype == torch.uint8)
-        if d.out_e4m3 and (s.amax is None or s.scale is None):
+        if B == 1:
+            xb = ob = 0
+        if L == 1:
+            xt = ot = 0
+        if H == 1:
+            xh = oh = 0
+        amax, scale, weight, table = s.amax, s.scale, s.weight, s.table
+        if codes and (amax is None or scale is None):
             raise ValueError("E4M3 codes need amax and scale")
-        d.weight = _vector(s.weight, D, "weight")
-        d.amax, d.scale_out = _vector(s.amax, 1, "amax"), _vector(s.scale, 1, "scale")
-        if table is not None:
-            ts = table.stride()
-            r = 2 * table.shape[-2] if table.dim() >= 3 else 0
-            if table.dtype != torch.float32 or table.dim() not in (3, 4) or table.shape[-1] != 2 or \
-                    table.shape[-3] != L or (table.dim() == 4 and table.shape[0] != B):
+        if table is None:
+            table_at = table_b = 0
+        elif table is not seen or L != seen_rows:
+            shape, ts = table.shape, table.stride()
+            if table.dtype is not _F32 or len(shape) < 3 or shape[-1] != 2 or (shape[:-2] != (L,) and shape[:-2] != (B, L)):
                 raise ValueError(f"table must be float32 [{L}, R/2, 2] or [{B}, {L}, R/2, 2]")
+            r = 2 * shape[-2]
             if ts[-1] != 1 or (r > 2 and ts[-2] != 2) or (L > 1 and ts[-3] != r):
                 raise ValueError("the rows of a table must be contiguous")
             if rotary and r != rotary:
                 raise ValueError("the tables of a call have the same number of pairs")
-            rotary = r
-            d.table, d.table_stride_b = table.data_ptr(), (ts[0] if table.dim() == 4 and B > 1 else 0)
-    _check(load().qattn_norm_rope(io, n, B, D, rotary, int(bool(interleaved)), float(eps), _DTYPES[dtype],
-                                  _stream(stream)), "qattn_norm_rope")
+            if table.get_device() != index:
+                _same_device(index, table=table)
+            rotary, seen, seen_rows = r, table, L
+            table_at, table_b = table.data_ptr(), (ts[0] if len(shape) == 4 and B > 1 else 0)
+        else:
+            table_at, table_b = seen_at
+        if table is not None:
+            seen_at = table_at, table_b
+        _NORM_ROPE_IO.pack_into(io, at, x.data_ptr(), out.data_ptr(),
+                                0 if weight is None else _vector(weight, D, index, "weight"), table_at,
+                                0 if amax is None else _vector(amax, 1, index, "amax"),
+                                0 if scale is None else _vector(scale, 1, index, "scale"),
+                                xb, xt, xh, ob, oh, ot, table_b, H, L, codes)
+        at += _NORM_ROPE_IO.size
+    _check(load().qattn_norm_rope(bytes(io), n, B, D, rotary, bool(interleaved), eps, _DTYPES[dtype], handle),
+           "qattn_norm_rope")
 
 
 def _codes(t, what):
-    if t.dtype != torch.int8:
+    if t.dtype is not _I8:
         raise ValueError(f"{what} must be int8, got {t.dtype}")
     return t.data_ptr()
 
@@ -477,10 +518,12 @@ def quantize_int8_rows(x, out, scale, stream=None):
     out int8 [M, K] (row stride a multiple of 16), scale float32 [M] = amax / 127."""
     dtype = _act(x, "x")
     M, K = x.shape
-    ldx, ldo = _rows(x, (M, K), "x"), _rows(out, (M, K), "out", 16)
-    _on_device(x.device, stream, out=out, scale=scale)
+    ldx, ldo = _rows(x, M, K, "x"), _rows(out, M, K, "out", 16)
+    index = x.get_device()
+    _same_device(index, out=out)
+    handle = _launch_stream(index, stream)
     _check(load().qattn_quantize_int8_rows(x.data_ptr(), ldx, dtype, M, K, _codes(out, "out"), ldo,
-                                           _vector(scale, M, "scale"), _stream(stream)), "qattn_quantize_int8_rows")
+                                           _vector(scale, M, index, "scale"), handle), "qattn_quantize_int8_rows")
 
 
 def gemm_int8(a8, b8, y, s_a, s_b, bias=None, stream=None):
@@ -491,27 +534,33 @@ def gemm_int8(a8, b8, y, s_a, s_b, bias=None, stream=None):
     if a8.dim() != 2:
         raise ValueError("a8 must be [M, K]")
     K = a8.shape[1]
-    lda, ldb, ldy = _rows(a8, (M, K), "a8", 16), _rows(b8, (N, K), "b8", 16), _rows(y, (M, N), "y")
-    _on_device(y.device, stream, a8=a8, b8=b8, s_a=s_a, s_b=s_b, bias=bias)
+    lda, ldb, ldy = _rows(a8, M, K, "a8", 16), _rows(b8, N, K, "b8", 16), _rows(y, M, N, "y")
+    index = y.get_device()
+    _same_device(index, a8=a8, b8=b8)
+    handle = _launch_stream(index, stream)
     _check(load().qattn_gemm_int8(_codes(a8, "a8"), lda, _codes(b8, "b8"), ldb, y.data_ptr(), ldy, dtype, M, N, K,
-                                  _vector(s_a, M, "s_a"), _vector(s_b, N, "s_b"), _vector(bias, N, "bias"),
-                                  _stream(stream)), "qattn_gemm_int8")
+                                  _vector(s_a, M, index, "s_a"), _vector(s_b, N, index, "s_b"),
+                                  _vector(bias, N, index, "bias"), handle), "qattn_gemm_int8")
 
 
 def linear_int8(x, x8, s_x, w8, s_w, y, bias=None, stream=None):
     """quantize_int8_rows(x, x8, s_x) and gemm_int8(x8, w8, y, s_x, s_w, bias) in one call, the second
-    launch starting while the first runs."""
+    launch starting while the first runs (one launch for one or two tokens)."""
     dtype = _act(x, "x")
     M, K = x.shape
     N = w8.shape[0]
-    if y.dtype != x.dtype:
+    if y.dtype is not x.dtype:
         raise ValueError("y must have x's type")
-    ldx, ld8 = _rows(x, (M, K), "x"), _rows(x8, (M, K), "x8", 16)
-    ldw, ldy = _rows(w8, (N, K), "w8", 16), _rows(y, (M, N), "y")
-    _on_device(x.device, stream, x8=x8, s_x=s_x, w8=w8, s_w=s_w, y=y, bias=bias)
-    _check(load().qattn_linear_int8(x.data_ptr(), ldx, dtype, M, N, K, _codes(x8, "x8"), ld8, _vector(s_x, M, "s_x"),
-                                    _codes(w8, "w8"), ldw, _vector(s_w, N, "s_w"), _vector(bias, N, "bias"),
-                                    y.data_ptr(), ldy, _stream(stream)), "qattn_linear_int8")
+    ldx, ld8 = _rows(x, M, K, "x"), _rows(x8, M, K, "x8", 16)
+    ldw, ldy = _rows(w8, N, K, "w8", 16), _rows(y, M, N, "y")
+    index = x.get_device()
+    if x8.get_device() != index or w8.get_device() != index or y.get_device() != index:
+        _same_device(index, x8=x8, w8=w8, y=y)
+    handle = _launch_stream(index, stream)
+    _check(load().qattn_linear_int8(x.data_ptr(), ldx, dtype, M, N, K, _codes(x8, "x8"), ld8,
+                                    _vector(s_x, M, index, "s_x"), _codes(w8, "w8"), ldw,
+                                    _vector(s_w, N, index, "s_w"), _vector(bias, N, index, "bias"),
+                                    y.data_ptr(), ldy, handle), "qattn_linear_int8")
 
 
 def _scales(s_q, s_k, s_v):

@@ -71,6 +71,26 @@ __device__ __forceinline__ uint2 codes8(const uint32_t (&w)[4], const RowCode& k
   return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
 
+// Scale of a row whose largest magnitude has the bit pattern mx, and how its codes are formed.
+struct RowScale {
+  float scale;
+  bool finite;
+  RowCode code;
+};
+template <bool FP16>
+__device__ __forceinline__ RowScale row_scale_of(uint32_t mx) {
+  RowScale s;
+  s.finite = mx < (FP16 ? 0x7C00u : 0x7F80u);
+  float amax = from16<FP16>(mx);
+  s.scale = !s.finite ? __int_as_float(0x7FFFFFFF) : mx == 0 ? 1.0f : __fdiv_rn(amax, 127.0f);
+  if (mx == 0) amax = 1.0f;
+  const float p2 = scale_pow2(amax), c127 = 127.0f * p2;
+  amax *= p2;
+  const float r = __frcp_rn(amax);
+  s.code = {pack_f32x2(c127, c127), pack_f32x2(r, r), pack_f32x2(-amax, -amax)};
+  return s;
+}
+
 // Eight elements of a row from `at` (a multiple of 8); those past K read as zero.
 template <bool VEC>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int at, int K) {
@@ -126,22 +146,16 @@ __global__ void __launch_bounds__(256) k_quant_int8_rows(const uint16_t* __restr
     for (int i = 1; i < WARPS; ++i) mx = max(mx, part[sub * WARPS + i]);
   }
   if (m >= M || !QATTN_IN_BOUNDS(err, m >= 0)) return;
-  const bool finite = mx < (FP16 ? 0x7C00u : 0x7F80u);
-  float amax = from16<FP16>(mx);
+  const RowScale rs = row_scale_of<FP16>(mx);
   if (tid == 0) {
-    if (!finite) atomicExch(err, DEV_ERR_NONFINITE);
-    scale[m] = !finite ? __int_as_float(0x7FFFFFFF) : mx == 0 ? 1.0f : __fdiv_rn(amax, 127.0f);
+    if (!rs.finite) atomicExch(err, DEV_ERR_NONFINITE);
+    scale[m] = rs.scale;
   }
-  if (mx == 0) amax = 1.0f;
-  const float p2 = scale_pow2(amax), c127 = 127.0f * p2;
-  amax *= p2;
-  const float r = __frcp_rn(amax);
-  const RowCode k{pack_f32x2(c127, c127), pack_f32x2(r, r), pack_f32x2(-amax, -amax)};
   int8_t* orow = out + static_cast<int64_t>(m) * ldo;
   auto put = [&](const uint4& u, int at) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     uint2 c = make_uint2(0u, 0u);
-    if (finite) c = codes8<FP16>(w, k);
+    if (rs.finite) c = codes8<FP16>(w, rs.code);
     if (at + 8 <= K) {
       *reinterpret_cast<uint2*>(orow + at) = c;
     } else {
@@ -168,26 +182,204 @@ static void launch_rows(const void* x, int64_t ldx, bool fp16, bool vec, int M, 
   else k_quant_int8_rows<T, NV, false, false><<<grid, 256, 0, stream>>>(p, ldx, M, K, out, ldo, scale, err);
 }
 
-// A warp for rows of up to 1024 elements, 128 threads up to 4096, a block beyond (in registers up
-// to 16384).
+// Threads and registers by the row's length: what holds a row with the fewest idle registers (12288 elements on
+// 256 x 6 against 256 x 8 vectors: 4608 rows 28.0 / 30.2 us); with few rows, more threads for each (64 rows of 4096:
+// 2.0 us on 256 threads, 2.5 on 128; 8704 rows 21.3 / 20.6).
 cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, int K, int8_t* out,
                                    int64_t ldo, float* scale, int* err, cudaStream_t stream) {
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
   if (K <= 1024) launch_rows<32, 4>(x, ldx, fp16, vec, M, K, out, ldo, scale, err, stream);
+  else if (K <= 4096 && M <= 512) launch_rows<256, 2>(x, ldx, fp16, vec, M, K, out, ldo, scale, err, stream);
   else if (K <= 4096) launch_rows<128, 4>(x, ldx, fp16, vec, M, K, out, ldo, scale, err, stream);
   else if (K <= 8192) launch_rows<256, 4>(x, ldx, fp16, vec, M, K, out, ldo, scale, err, stream);
+  else if (K <= 12288) launch_rows<256, 6>(x, ldx, fp16, vec, M, K, out, ldo, scale, err, stream);
   else launch_rows<256, 8>(x, ldx, fp16, vec, M, K, out, ldo, scale, err, stream);
   return cudaGetLastError();
 }
 
 // -------------------------------------------------------------------------------------------
+// Single tokens (one or two): the weights are read once with plain 16-byte loads and multiplied with dp4a, which asks
+// for the first weights sooner than a copy engine, tensor memory and a cluster that have to be set up first.  A warp takes
+// ROWS weight rows at a time over all of K, eight chunks of 512 bytes in flight; the tokens' codes
+// lie in shared memory.  One row where every row then has its warp (N <= 32 for each SM), else two, which halves the
+// reads of the codes: 4096 x 11008 10.7 / 11.9 us, 4096 x 4096 5.7 / 6.0, 6144 x 4096 7.9 / 7.3, 18944 x 4096 14.3 / 14.1.
+// (More tokens are faster with the cluster kernel: four at 6144 x 4096 13.3 against 11.4.)  QUANT: every block quantizes the tokens itself (a few KB, from L2) while its first weights are on
+// their way, and block 0 also writes the codes and scales out, so that a linear layer is one launch.
+// -------------------------------------------------------------------------------------------
+namespace one {
+constexpr int THREADS = 512, WARPS = THREADS / 32, BLOCKS = 2;   // per SM
+constexpr int MOST_TOKENS = 2;
+constexpr int MOST_BYTES = 96 * 1024;              // of codes in shared memory
+}  // namespace one
+
+__device__ __forceinline__ uint4 load_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// 16 codes of a row from byte `at`, those past K zero.
+__device__ __forceinline__ uint4 load_codes16(const int8_t* row, int at, int K) {
+  if (at + 16 <= K) return load_stream16(row + at);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (at + j < K) w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[at + j])) << (8 * (j & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct OneArgs {
+  const uint16_t* x;                               // QUANT: the tokens, and where their codes and scales go
+  int64_t ldx;
+  int8_t* x8;                                      // else the codes
+  int64_t ldx8;
+  float* s_x;
+  const int8_t* w;
+  int64_t ldw;
+};
+
+template <int TOK, int ROWS, bool FP16, bool QUANT, bool VEC>
+__global__ void __launch_bounds__(one::THREADS, one::BLOCKS)
+    k_gemm_int8_one(const __grid_constant__ OneArgs o, const __grid_constant__ GemmInt8Args args) {
+  using namespace one;
+  constexpr int CHUNKS = 8 / ROWS;
+  extern __shared__ __align__(16) uint8_t one_codes[];   // [TOK][kpad]
+  __shared__ uint32_t part[WARPS][TOK];
+  __shared__ float scales[TOK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int K = args.K, kpad = (K + 15) / 16 * 16, steps = (kpad + 511) / 512;
+  int n = (static_cast<int>(blockIdx.x) * WARPS + warp) * ROWS;
+
+  uint4 w[ROWS][CHUNKS];
+  auto load = [&](int first) {                     // chunks first .. first + CHUNKS - 1 of rows n ..
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int at = ((first + c) * 32 + lane) * 16;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        w[r][c] = make_uint4(0u, 0u, 0u, 0u);
+        if (at < K && n + r < args.N) w[r][c] = load_codes16(o.w + (n + r) * o.ldw, at, K);
+      }
+    }
+  };
+  load(0);
+
+  if (QUANT) {
+    uint32_t mx[TOK];
+#pragma unroll
+    for (int m = 0; m < TOK; ++m) {
+      uint32_t m2 = 0;
+      if (m < args.M) {
+        const uint16_t* row = o.x + m * o.ldx;
+        for (int at = threadIdx.x * 8; at < K; at += THREADS * 8) {
+          const uint4 v = load8<VEC>(row, at, K);
+          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        }
+      }
+      mx[m] = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));
+      if (lane == 0) part[warp][m] = mx[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < TOK; ++m) {
+      uint32_t top = part[0][m];
+#pragma unroll
+      for (int i = 1; i < WARPS; ++i) top = max(top, part[i][m]);
+      const RowScale rs = row_scale_of<FP16>(top);
+      if (threadIdx.x == 0) {
+        scales[m] = rs.scale;
+        if (blockIdx.x == 0 && m < args.M) {
+          o.s_x[m] = rs.scale;
+          if (!rs.finite) atomicExch(args.err, DEV_ERR_NONFINITE);
+        }
+      }
+      const uint16_t* row = o.x + m * o.ldx;
+      for (int at = threadIdx.x * 8; at < kpad; at += THREADS * 8) {
+        uint2 c = make_uint2(0u, 0u);
+        if (m < args.M && at < K && rs.finite) {
+          const uint4 v = load8<VEC>(row, at, K);
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          c = codes8<FP16>(e, rs.code);
+        }
+        *reinterpret_cast<uint2*>(one_codes + m * kpad + at) = c;
+        if (blockIdx.x == 0 && m < args.M) {
+          int8_t* to = o.x8 + m * o.ldx8 + at;
+          if (at + 8 <= K) {
+            *reinterpret_cast<uint2*>(to) = c;
+          } else {
+            for (int j = 0; at + j < K; ++j)
+              to[j] = static_cast<int8_t>((j < 4 ? c.x >> (8 * j) : c.y >> (8 * (j - 4))) & 0xFFu);
+          }
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < TOK; ++m) {
+      if (threadIdx.x == 0) scales[m] = m < args.M ? args.s_a[m] : 0.0f;
+      for (int at = threadIdx.x * 16; at < kpad; at += THREADS * 16)
+        *reinterpret_cast<uint4*>(one_codes + m * kpad + at) =
+            m < args.M ? load_codes16(o.x8 + m * o.ldx8, at, K) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __syncthreads();
+
+  for (; n < args.N; n += static_cast<int>(gridDim.x) * WARPS * ROWS) {
+    int acc[ROWS][TOK];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int m = 0; m < TOK; ++m) acc[r][m] = 0;
+    for (int first = 0; first < steps; first += CHUNKS) {
+      if (first > 0 || n >= static_cast<int>(gridDim.x) * WARPS * ROWS) load(first);   // the first is here already
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        const int at = ((first + c) * 32 + lane) * 16;
+        if (at < kpad) {
+#pragma unroll
+          for (int m = 0; m < TOK; ++m) {
+            const uint4 x = *reinterpret_cast<const uint4*>(one_codes + m * kpad + at);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+              int a = acc[r][m];
+              a = __dp4a(static_cast<int>(w[r][c].x), static_cast<int>(x.x), a);
+              a = __dp4a(static_cast<int>(w[r][c].y), static_cast<int>(x.y), a);
+              a = __dp4a(static_cast<int>(w[r][c].z), static_cast<int>(x.z), a);
+              acc[r][m] = __dp4a(static_cast<int>(w[r][c].w), static_cast<int>(x.w), a);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+#pragma unroll
+      for (int m = 0; m < TOK; ++m) {
+        const int a = __reduce_add_sync(0xFFFFFFFFu, acc[r][m]);
+        if (lane == r * TOK + m && n + r < args.N && m < args.M && QATTN_IN_BOUNDS(args.err, n + r < args.N)) {
+          const float b = args.bias ? __ldg(args.bias + n + r) : 0.0f;
+          static_cast<uint16_t*>(args.y)[m * args.ldy + n + r] =
+              to16<FP16>(fmaf(static_cast<float>(a) * scales[m], __ldg(args.s_b + n + r), b));
+        }
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------------------------------------
 // Few tokens: bound by streaming the weights once.  One CTA takes 128 weight rows (the
-// MMA's M = 128, the TMEM lanes) against a tile of tokens (N = TOK, 16 to 256) over a range of K; the
+// MMA's M = 128, the TMEM lanes) against a tile of tokens (N = TOK, 16 to 64) over a range of K; the
 // CTAs of a cluster share the 128 rows and cut K, so that a narrow layer still keeps every SM
-// loading.  int32 partial sums meet through distributed shared memory: exact, so neither the cut nor
-// the order changes a result, and no workspace or atomics are needed.
-//   warp 0      TMA producer; the weights of the first stages are requested before the wait for the
-//               preceding grid (the quantize writes only the activations)
+// loading.  int32 partial sums meet in distributed shared memory: exact, so neither the cut nor
+// the order changes a result, and no workspace or atomics are needed.  Groups of four tokens go round the CTAs; every
+// CTA sends its sums of a group to the owner with asynchronous stores that count on the owner's barrier, so that
+// nobody waits for the whole cluster at the end (two cluster barriers and the loads between them took 2 us).
+//   warp 0      TMA producer of the weights: it sets the barriers up and starts without waiting for the other
+//               warps or for the preceding grid (the quantize writes only the activations)
+//   warp 10     TMA producer of the tokens' codes (one thread issues a copy in about 100 clocks; two producers
+//               halve the time of a K block)
 //   warp 1      MMA issuer and TMEM owner
 //   warps 2-9   epilogue: lane = output channel, column = token; two warps for each TMEM lane quarter,
 //               each with every other group of eight tokens
@@ -197,23 +389,29 @@ cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, 
 namespace few {
 constexpr int BN = 128;                  // weight rows per CTA
 constexpr int BK = 128;
-constexpr int THREADS = 320;
+constexpr int THREADS = 352;
 constexpr int TILE_W = BN * BK;
+constexpr int MOST_STAGES = 10;
 template <int TOK>
 struct Smem {
   static constexpr int TILE_X = TOK * BK;
   static constexpr int STAGE = TILE_W + TILE_X;
-  static constexpr int STAGES = (TOK <= 128 ? 104 : 200) * 1024 / STAGE;   // up to 128 tokens: two CTAs an SM
-  static constexpr int OFF_W = 0, OFF_X = STAGES * TILE_W;
-  static constexpr int OFF_BAR = OFF_X + STAGES * TILE_X;
-  static constexpr int NBARS = 2 * STAGES + 2;                 // full, empty, accumulator, drain
+  // full, empty, accumulator, drain, partial sums
+  static constexpr int NBARS = 2 * MOST_STAGES + 3;
+  static constexpr int OFF_BAR = 0;
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBARS;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int OFF_SA = (OFF_ABORT + 4 + 15) / 16 * 16;   // the tile's token scales
-  static constexpr int ALLOC = OFF_SA + 4 * TOK + 1024;
-  static constexpr int ROW = TOK + 4;                          // words of a channel's partial sums (no conflicts)
-  static_assert(ROW * 128 * 4 <= STAGES * STAGE, "partial sums reuse the stages");
-  static_assert(TILE_X % 1024 == 0, "alignment");
+  static constexpr int OFF_RED = OFF_SA + 4 * TOK;                // partial sums: [peer][group][channel] of 16 bytes
+  // a CTA owns up to ceil(TOK / 4 / split) groups from split peers, 2 KB each
+  static constexpr int RED = (TOK / 4 + 8) * 2048;
+  static constexpr int OFF_STAGES = (OFF_RED + RED + 1023) / 1024 * 1024;
+  static constexpr int bytes(int stages) { return OFF_STAGES + stages * STAGE + 1024; }
+  // one CTA an SM with all it can hold in flight, or two
+  static constexpr int ALONE = (226 * 1024 - OFF_STAGES - 1024) / STAGE < MOST_STAGES
+                                   ? (226 * 1024 - OFF_STAGES - 1024) / STAGE : MOST_STAGES;
+  static constexpr int SHARED = (112 * 1024 - OFF_STAGES - 1024) / STAGE;
+  static_assert(TILE_X % 1024 == 0 && SHARED >= 2, "alignment and stages");
 };
 }  // namespace few
 
@@ -229,7 +427,7 @@ __global__ void __launch_bounds__(few::THREADS, 2)
                     const __grid_constant__ GemmInt8Args args) {
   using namespace few;
   using S = Smem<TOK>;
-  constexpr int STAGES = S::STAGES;
+  const int stages = args.stages;
   constexpr uint32_t TMEM_COLS = TOK < 32 ? 32 : TOK;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -249,69 +447,91 @@ __global__ void __launch_bounds__(few::THREADS, 2)
 
   const uint32_t bar0 = base_u32 + S::OFF_BAR;
   auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
-  constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC = 2 * STAGES, B_DRAIN = B_ACC + 1;
+  constexpr int B_FULL = 0, B_EMPTY = MOST_STAGES, B_ACC = 2 * MOST_STAGES, B_DRAIN = B_ACC + 1, B_RED = B_ACC + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + S::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OFF_TMEM);
   float* s_tok = reinterpret_cast<float*>(base + S::OFF_SA);
-  const int pre = nkb < STAGES ? nkb : STAGES;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) { mbar_init(BAR(B_FULL + i), 1); mbar_init(BAR(B_EMPTY + i), 1); }
-    mbar_init(BAR(B_ACC), 1);
-    mbar_init(BAR(B_DRAIN), 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    fence_proxy_async();
-    // the producer's first weights are on their way while TMEM is allocated and the CTA assembles
-    (void)QATTN_IN_BOUNDS(args.err, n0 < args.N && m0 < args.M && nkb >= 1 && kb0 + nkb <= kblocks);
-    for (int u = 0; u < pre; ++u) {
-      mbar_arrive_expect_tx(BAR(B_FULL + u), S::STAGE);
-      tma_load_2d(base_u32 + S::OFF_W + u * TILE_W, &tm_w, BAR(B_FULL + u), (kb0 + u) * BK, n0);
-    }
-  }
-  if (warp == 1) {
-    tmem_alloc(base_u32 + S::OFF_TMEM, TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const int groups = (tokens + 3) / 4, per = (groups - 1) / split + 1;      // of the tile; of an owner, at most
+  const int mine = (groups - rank + split - 1) / split;                     // of this CTA: rank, rank + split, ..
+  const uint32_t stage0 = base_u32 + S::OFF_STAGES;
   const uint64_t tlim = args.timeout_ns;
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int i = 0; i < stages; ++i) { mbar_init(BAR(B_FULL + i), 1); mbar_init(BAR(B_EMPTY + i), 1); }
+      mbar_init(BAR(B_ACC), 1);
+      mbar_init(BAR(B_DRAIN), 1);
+      mbar_init(BAR(B_RED), 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_proxy_async();
+      if (split > 1 && mine > 0) mbar_arrive_expect_tx(BAR(B_RED), static_cast<uint32_t>(mine * split) * 2048u);
+      (void)QATTN_IN_BOUNDS(args.err, n0 < args.N && m0 < args.M && nkb >= 1 && kb0 + nkb <= kblocks);
+    }
+    __syncwarp();
+    asm volatile("bar.arrive 2, 352;" ::: "memory");   // the barriers are ready; nothing else is needed here
+  } else {
+    if (warp == 1) {
+      tmem_alloc(base_u32 + S::OFF_TMEM, TMEM_COLS);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 2, 352;" ::: "memory");
+    tc_fence_after();
+  }
+  if (split > 1) cluster_arrive();                 // this CTA's barriers are ready for its peers' sums
+  const uint32_t tmem = warp == 0 ? 0u : *tmem_slot;
 
   bool got = false;                                // epilogue threads: the accumulator is complete
   if (warp == 0) {
-    // ======================= TMA producer =======================
+    // ======================= TMA producer: weights =======================
+    if (elect_one()) {
+      int s = 0;
+      uint32_t phase = 1;                          // of the stage's use before; the first round passes at once
+      int u = 0;
+      for (; u < nkb; ++u) {
+        if (!mbar_wait(BAR(B_EMPTY + s), phase, tlim, abort_flag, args.err)) break;
+        mbar_arrive_expect_tx(BAR(B_FULL + s), S::STAGE);
+        tma_load_2d(stage0 + s * S::STAGE, &tm_w, BAR(B_FULL + s), (kb0 + u) * BK, n0);
+        if (++s == stages) { s = 0; phase ^= 1u; }
+      }
+      // every copy has landed before the CTA may exit (instant when healthy)
+      for (int j = u - 1; j >= 0 && j >= u - stages; --j)
+        mbar_drain(BAR(B_FULL + j % stages), (j / stages) & 1, tlim);
+    }
+  } else if (warp == 10) {
+    // ======================= TMA producer: tokens =======================
     if (elect_one()) {
       grid_wait_prior();
-      for (int u = 0; u < pre; ++u)
-        tma_load_2d(base_u32 + S::OFF_X + u * S::TILE_X, &tm_x, BAR(B_FULL + u), (kb0 + u) * BK, m0);
-      int u = pre;
+      int s = 0;
+      uint32_t phase = 1;
+      int u = 0;
       for (; u < nkb; ++u) {
-        const int s = u % STAGES;
-        if (!mbar_wait(BAR(B_EMPTY + s), ((u / STAGES) - 1) & 1, tlim, abort_flag, args.err)) break;
-        mbar_arrive_expect_tx(BAR(B_FULL + s), S::STAGE);
-        tma_load_2d(base_u32 + S::OFF_W + s * TILE_W, &tm_w, BAR(B_FULL + s), (kb0 + u) * BK, n0);
-        tma_load_2d(base_u32 + S::OFF_X + s * S::TILE_X, &tm_x, BAR(B_FULL + s), (kb0 + u) * BK, m0);
+        if (!mbar_wait(BAR(B_EMPTY + s), phase, tlim, abort_flag, args.err)) break;
+        tma_load_2d(stage0 + s * S::STAGE + TILE_W, &tm_x, BAR(B_FULL + s), (kb0 + u) * BK, m0);
+        if (++s == stages) { s = 0; phase ^= 1u; }
       }
-      for (int j = u - 1; j >= 0 && j >= u - STAGES; --j)
-        mbar_drain(BAR(B_FULL + j % STAGES), (j / STAGES) & 1, tlim);
+      // every copy has landed before the CTA may exit (instant when healthy)
+      for (int j = u - 1; j >= 0 && j >= u - stages; --j)
+        mbar_drain(BAR(B_FULL + j % stages), (j / stages) & 1, tlim);
     }
   } else if (warp == 1) {
     // ======================= MMA issuer =======================
     if (elect_one()) {
       constexpr uint32_t IDESC = idesc_s8_s32(BN, TOK);
       bool ok = true;
+      int s = 0;
+      uint32_t phase = 0;
       for (int u = 0; u < nkb; ++u) {
-        const int s = u % STAGES;
-        ok = mbar_wait(BAR(B_FULL + s), (u / STAGES) & 1, tlim, abort_flag, args.err);
+        ok = mbar_wait(BAR(B_FULL + s), phase, tlim, abort_flag, args.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t w_s = base_u32 + S::OFF_W + s * TILE_W, x_s = base_u32 + S::OFF_X + s * S::TILE_X;
+        const uint32_t w_s = stage0 + s * S::STAGE, x_s = stage0 + s * S::STAGE + TILE_W;
 #pragma unroll
         for (int kk = 0; kk < BK / 32; ++kk)
           mma_i8_ss(tmem, smem_desc(w_s + kk * 32, 16, 1024, 2u), smem_desc(x_s + kk * 32, 16, 1024, 2u),
                     IDESC, (u > 0 || kk > 0) ? 1u : 0u);
         mma_commit(BAR(B_EMPTY + s));
+        if (++s == stages) { s = 0; phase ^= 1u; }
       }
       if (ok) mma_commit(BAR(B_ACC));
       mma_commit(BAR(B_DRAIN));
@@ -347,7 +567,7 @@ __global__ void __launch_bounds__(few::THREADS, 2)
           if (c + e < tokens && QATTN_IN_BOUNDS(args.err, m0 + c + e < args.M)) y[(c + e) * args.ldy] = o[e];
       }
     };
-    int* part = reinterpret_cast<int*>(base) + r * S::ROW;      // the stages are free: every MMA has completed
+    if (split > 1) cluster_wait();                 // the peers' barriers are ready
     if (got) {
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -356,49 +576,44 @@ __global__ void __launch_bounds__(few::THREADS, 2)
         uint32_t v[8];
         tmem_ld8(acc + c, v);
         tmem_wait_ld();
-        if (split > 1) {
-          *reinterpret_cast<uint4*>(part + c) = make_uint4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<uint4*>(part + c + 4) = make_uint4(v[4], v[5], v[6], v[7]);
-        } else {
-          const int a0[4] = {static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3])};
-          const int a1[4] = {static_cast<int>(v[4]), static_cast<int>(v[5]), static_cast<int>(v[6]), static_cast<int>(v[7])};
-          put4(a0, c);
-          put4(a1, c + 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int g = c / 4 + j;
+          const int a[4] = {static_cast<int>(v[4 * j]), static_cast<int>(v[4 * j + 1]), static_cast<int>(v[4 * j + 2]),
+                            static_cast<int>(v[4 * j + 3])};
+          if (split == 1) {
+            put4(a, c + 4 * j);
+          } else if (g < groups) {
+            const int owner = g % split;
+            st_async_v4(mapa_shared(base_u32 + S::OFF_RED + static_cast<uint32_t>(((rank * per + g / split) * 128 + r) * 16),
+                                    static_cast<uint32_t>(owner)),
+                        a, mapa_shared(BAR(B_RED), static_cast<uint32_t>(owner)));
+          }
         }
       }
-    }
-    if (split > 1) {
-      tc_fence_before();
-      cluster_sync();                              // partial sums of every CTA are in shared memory
-      if (got) {
-        // groups of four tokens go round the cluster's CTAs; all peers' loads of a group are in flight
-        // together
-        for (int g = rank + half * split; 4 * g < tokens; g += 2 * split) {
-          const uint32_t at = smem_u32(part + 4 * g);
-          int4 v[8];
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            if (p < split) v[p] = ld_cluster_v4(mapa_shared(at, static_cast<uint32_t>(p)));
-          int a[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-          for (int p = 1; p < 8; ++p)
-            if (p < split) { a[0] += v[p].x; a[1] += v[p].y; a[2] += v[p].z; a[3] += v[p].w; }
-          put4(a, 4 * g);
+      if (split > 1 && mine > 0) {
+        got = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_RED), 0, tlim, abort_flag, args.err));
+        for (int i = half; got && i < mine; i += 2) {
+          int a[4] = {0, 0, 0, 0};
+          for (int p = 0; p < split; ++p) {
+            const int4 v = *reinterpret_cast<const int4*>(base + S::OFF_RED + ((p * per + i) * 128 + r) * 16);
+            a[0] += v.x;
+            a[1] += v.y;
+            a[2] += v.z;
+            a[3] += v.w;
+          }
+          put4(a, 4 * (i * split + rank));
         }
       }
     }
   }
 
-  if (split > 1) {
-    if (warp < 2) {
-      tc_fence_before();
-      cluster_sync();                              // with the epilogue's first
-    }
-    cluster_sync();                                // the peers have read this CTA's sums
-  } else {
-    tc_fence_before();
-    __syncthreads();
-  }
+  if (split > 1 && (warp < 2 || warp == 10)) cluster_wait();
+  tc_fence_before();
+  __syncthreads();
+  // A CTA that has given up keeps its shared memory until its peers have exited or given up too: their sums may
+  // still be on their way here.  (The flag is the same for every thread: its writers are past the barrier.)
+  if (split > 1 && *abort_flag) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
@@ -659,12 +874,12 @@ static bool make_map_rows(CUtensorMap* map, const void* ptr, int rows, int K, in
 }
 
 template <class K>
-static cudaError_t launch_ex(K kernel, DeviceOnce& once, dim3 grid, unsigned cluster, int threads, int smem,
-                             bool early, cudaStream_t stream, const CUtensorMap& a, const CUtensorMap& b,
+static cudaError_t launch_ex(K kernel, DeviceOnce& once, dim3 grid, unsigned cluster, int threads, int most_smem,
+                             int smem, bool early, cudaStream_t stream, const CUtensorMap& a, const CUtensorMap& b,
                              const GemmInt8Args& args) {
   const void* fn = reinterpret_cast<const void*>(kernel);
-  if (once.get([fn, smem] {
-        return static_cast<int>(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (once.get([fn, most_smem] {
+        return static_cast<int>(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem));
       }) != static_cast<int>(cudaSuccess))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -689,27 +904,59 @@ static cudaError_t launch_ex(K kernel, DeviceOnce& once, dim3 grid, unsigned clu
   return cudaLaunchKernelEx(&cfg, kernel, a, b, args);
 }
 
-// How many CTAs share 128 weight rows and a token tile: enough to give every SM a CTA, with at least four
-// K blocks each.
+// Clusters of `split` CTAs that are resident at once at one CTA an SM.  They do not cross the SMs' groups, so there may be
+// fewer than SMs / split: 48 clusters of three take two rounds on 148 SMs.
+template <int TOK, bool FP16>
+static int few_resident(int split, int num_sms) {
+  constexpr int SMEM = few::Smem<TOK>::bytes(few::Smem<TOK>::ALONE);
+  cudaFuncSetAttribute(k_gemm_int8_few<TOK, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms / split * split));
+  cfg.blockDim = dim3(few::THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(split);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k_gemm_int8_few<TOK, FP16>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+// CTAs that share 128 weight rows and a token tile: as many as keep all tiles resident at one CTA an SM, with at
+// least four K blocks each.  16 tokens, K = 4096, splits 1 / 2 / 3 / 4 / 8: N = 4096 9.9 / 9.0 / 8.5 / 8.1 / 8.6 us,
+// 6144 10.3 / 9.8 / 15.3 / 9.8 / 11.5, 1024 8.6 / 7.5 / 6.8 / 6.1 / 5.3, 12288 13.1 / 14.5 / 17.7 / 16.1 / 18.9.
+template <int TOK, bool FP16>
 static int few_split(int64_t tiles, int K, int num_sms) {
+  static DeviceOnce resident[9];
   const int kblocks = (K + few::BK - 1) / few::BK;
-  int64_t split = num_sms / tiles;
-  if (split > kblocks / 4) split = kblocks / 4;
-  return split < 1 ? 1 : split > 8 ? 8 : static_cast<int>(split);
+  for (int split = 8; split > 1; --split) {
+    if (split > kblocks / 4 || tiles * split > num_sms) continue;
+    if (tiles <= resident[split].get([split, num_sms] { return few_resident<TOK, FP16>(split, num_sms); })) return split;
+  }
+  return 1;
 }
 
 template <int TOK, bool FP16>
 static cudaError_t launch_few(const int8_t* x, int64_t ldx, const int8_t* w, int64_t ldw, const GemmInt8Args& a,
                               int num_sms, bool early, cudaStream_t stream) {
   static DeviceOnce once;
+  using S = few::Smem<TOK>;
   CUtensorMap mw, mx;
   if (!make_map_rows(&mw, w, a.N, a.K, ldw, few::BN) || !make_map_rows(&mx, x, a.M, a.K, ldx, TOK))
     return cudaErrorInvalidValue;
   const int64_t tiles = (static_cast<int64_t>(a.N) + few::BN - 1) / few::BN * ((a.M + TOK - 1) / TOK);
   GemmInt8Args b = a;
-  b.split = few_split(tiles, a.K, num_sms);
+  b.split = few_split<TOK, FP16>(tiles, a.K, num_sms);
+  b.stages = tiles * b.split <= num_sms ? S::ALONE : S::SHARED;
   return launch_ex(k_gemm_int8_few<TOK, FP16>, once, dim3(static_cast<unsigned>(tiles * b.split)),
-                   static_cast<unsigned>(b.split), few::THREADS, few::Smem<TOK>::ALLOC, early, stream, mw, mx, b);
+                   static_cast<unsigned>(b.split), few::THREADS, S::bytes(S::ALONE), S::bytes(b.stages), early, stream,
+                   mw, mx, b);
 }
 
 template <int BN, bool FP16>
@@ -736,7 +983,51 @@ static cudaError_t launch_pair(const int8_t* x, int64_t ldx, const int8_t* w, in
   const int64_t tiles = (static_cast<int64_t>(a.M) + pair8::BM - 1) / pair8::BM * ((a.N + BN - 1) / BN);
   const int pairs = tiles < most ? static_cast<int>(tiles) : most;
   return launch_ex(k_gemm_int8_pair<BN, FP16>, once, dim3(static_cast<unsigned>(2 * pairs)), 0, pair8::THREADS,
-                   pair8::Smem<BN>::ALLOC, early, stream, ma, mb, a);
+                   pair8::Smem<BN>::ALLOC, pair8::Smem<BN>::ALLOC, early, stream, ma, mb, a);
+}
+
+template <int TOK, int ROWS, bool FP16, bool QUANT, bool VEC>
+static cudaError_t launch_one_rows(const OneArgs& o, const GemmInt8Args& a, int num_sms, cudaStream_t stream) {
+  static DeviceOnce once;
+  const void* fn = reinterpret_cast<const void*>(k_gemm_int8_one<TOK, ROWS, FP16, QUANT, VEC>);
+  if (once.get([fn] {
+        return static_cast<int>(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, one::MOST_BYTES));
+      }) != static_cast<int>(cudaSuccess))
+    return cudaErrorInvalidValue;
+  const int per_block = one::WARPS * ROWS;
+  const int64_t blocks = (static_cast<int64_t>(a.N) + per_block - 1) / per_block, most = static_cast<int64_t>(num_sms) * one::BLOCKS;
+  k_gemm_int8_one<TOK, ROWS, FP16, QUANT, VEC><<<static_cast<unsigned>(blocks < most ? blocks : most), one::THREADS,
+                                           TOK * ((a.K + 15) / 16 * 16), stream>>>(o, a);
+  return cudaGetLastError();
+}
+
+template <int TOK, bool FP16, bool QUANT, bool VEC>
+static cudaError_t launch_one_as(const OneArgs& o, const GemmInt8Args& a, int num_sms, cudaStream_t stream) {
+  if (a.N <= num_sms * one::BLOCKS * one::WARPS) return launch_one_rows<TOK, 1, FP16, QUANT, VEC>(o, a, num_sms, stream);
+  return launch_one_rows<TOK, 2, FP16, QUANT, VEC>(o, a, num_sms, stream);
+}
+
+template <int TOK, bool QUANT>
+static cudaError_t launch_one(const OneArgs& o, const GemmInt8Args& a, int fp16, int num_sms, cudaStream_t stream) {
+  const bool vec = !QUANT || ((reinterpret_cast<uintptr_t>(o.x) & 15) == 0 && o.ldx % 8 == 0);
+  if (fp16 && vec) return launch_one_as<TOK, true, QUANT, true>(o, a, num_sms, stream);
+  if (vec) return launch_one_as<TOK, false, QUANT, true>(o, a, num_sms, stream);
+  if constexpr (QUANT) {
+    if (fp16) return launch_one_as<TOK, true, QUANT, false>(o, a, num_sms, stream);
+    return launch_one_as<TOK, false, QUANT, false>(o, a, num_sms, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// One or two tokens whose codes fit shared memory.
+static bool one_fits(int M, int K) {
+  return M <= one::MOST_TOKENS && static_cast<int64_t>(M) * ((K + 15) / 16 * 16) <= one::MOST_BYTES;
+}
+
+template <bool QUANT>
+static cudaError_t launch_one_m(const OneArgs& o, const GemmInt8Args& a, int fp16, int num_sms, cudaStream_t stream) {
+  if (a.M == 1) return launch_one<1, QUANT>(o, a, fp16, num_sms, stream);
+  return launch_one<2, QUANT>(o, a, fp16, num_sms, stream);
 }
 
 // Columns of a pair tile.  In us for a pair of SMs at 1.9 GHz: a K block of 128 takes 0.17, 0.19 and 0.26 for 64, 128
@@ -773,11 +1064,26 @@ static cudaError_t launch_any(const int8_t* x, int64_t ldx, const int8_t* w, int
   return launch_pair<256, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
 }
 
-cudaError_t launch_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb,
-                             const GemmInt8Args& a, int fp16, int num_sms, bool early,
-                             cudaStream_t stream) {
+static cudaError_t launch_codes(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb, const GemmInt8Args& a,
+                                int fp16, int num_sms, bool early, cudaStream_t stream) {
   return fp16 ? launch_any<true>(a8, lda, b8, ldb, a, num_sms, early, stream)
               : launch_any<false>(a8, lda, b8, ldb, a, num_sms, early, stream);
+}
+
+cudaError_t launch_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb, const GemmInt8Args& a,
+                             int fp16, int num_sms, cudaStream_t stream) {
+  if (one_fits(a.M, a.K))
+    return launch_one_m<false>({nullptr, 0, const_cast<int8_t*>(a8), lda, nullptr, b8, ldb}, a, fp16, num_sms, stream);
+  return launch_codes(a8, lda, b8, ldb, a, fp16, num_sms, false, stream);
+}
+
+cudaError_t launch_linear_int8(const void* x, int64_t ldx, int8_t* x8, int64_t ldx8, float* s_x, const int8_t* w8,
+                               int64_t ldw, const GemmInt8Args& a, int fp16, int num_sms, cudaStream_t stream) {
+  if (one_fits(a.M, a.K))
+    return launch_one_m<true>({static_cast<const uint16_t*>(x), ldx, x8, ldx8, s_x, w8, ldw}, a, fp16, num_sms, stream);
+  const cudaError_t e = launch_quant_int8_rows(x, ldx, fp16, a.M, a.K, x8, ldx8, s_x, a.err, stream);
+  if (e != cudaSuccess) return e;
+  return launch_codes(x8, ldx8, w8, ldw, a, fp16, num_sms, true, stream);
 }
 
 }  // namespace qattn

@@ -103,15 +103,14 @@ struct NormRopeArgs {
 bool plan_norm_rope(NormRopeArgs& a, int B, int num_sms, unsigned* grid);
 cudaError_t launch_norm_rope(const NormRopeArgs& a, unsigned grid, int pairs, int fp16, cudaStream_t stream);
 
-// 8-bit integer linear layers (gemm_int8.cu): per-row quantize of 16-bit X [M, K], and
-// Y [M, N] = (A8 [M, K] B8 [N, K]^T) * s_a[m] * s_b[n] (+ bias[n]); ld*: row strides in elements.
-// The quantize lets the next launch of its stream start early; early = true (GEMM) makes use of it:
-// the preceding launch of the stream must then be that quantize.
+// 8-bit integer linear layers (gemm_int8.cu): per-row quantize of 16-bit X [M, K];
+// Y [M, N] = (A8 [M, K] B8 [N, K]^T) * s_a[m] * s_b[n] (+ bias[n]); and both, where the GEMM starts while the quantize
+// runs (a.s_a is then s_x).  ld*: row strides in elements.
 cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, int K, int8_t* out,
                                    int64_t ldo, float* scale, int* err, cudaStream_t stream);
 struct GemmInt8Args {
   int M, N, K;
-  int split;                   // set by the launcher: CTAs that share a tile's K range
+  int split, stages;           // set by the launcher: CTAs that share a tile's K range, and their stages
   int64_t ldy;
   const float* s_a;
   const float* s_b;
@@ -120,9 +119,10 @@ struct GemmInt8Args {
   int* err;
   uint64_t timeout_ns;
 };
-cudaError_t launch_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb,
-                             const GemmInt8Args& a, int fp16, int num_sms, bool early,
-                             cudaStream_t stream);
+cudaError_t launch_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb, const GemmInt8Args& a,
+                             int fp16, int num_sms, cudaStream_t stream);
+cudaError_t launch_linear_int8(const void* x, int64_t ldx, int8_t* x8, int64_t ldx8, float* s_x, const int8_t* w8,
+                               int64_t ldw, const GemmInt8Args& a, int fp16, int num_sms, cudaStream_t stream);
 
 // The attention with P left unquantized (QATTN_FLAG_P_UNQUANTIZED, a debug path; attn_debug.cu):
 // dense (cu_seqlens == nullptr: B, H, L) or varlen (cu_seqlens, nseq, max_seqlen, total_tokens, H).

@@ -369,9 +369,11 @@ qattn_status qattn_rope_table(const void* pos_dev, qattn_pos_type pos_type, int6
     if (d < 2 || d % 2 != 0 || d > QATTN_ROPE_MAX_DIM) return QATTN_ERR_INVALID_ARG;
     if (!(theta[a] >= 1.0) || !(theta[a] < 1e300)) return QATTN_ERR_INVALID_ARG;
     if (pairs + d / 2 > QATTN_ROPE_MAX_DIM / 2) return QATTN_ERR_UNSUPPORTED;
-    for (int i = 0; i < d / 2; ++i, ++pairs) {
-      // turns per unit of position, theta^(-2 i / d) / (2 pi) <= 0.16, times 2^64
-      const long double turns = std::pow(static_cast<long double>(theta[a]), -2.0L * i / d) * 0.159154943091895335769L;
+    // turns per unit of position, theta^(-2 i / d) / (2 pi) <= 0.16, times 2^64: powers of the first ratio in
+    // 64 bits of mantissa (a power for each pair took 13 us of a 14 us call)
+    const long double ratio = std::pow(static_cast<long double>(theta[a]), -2.0L / d);
+    long double turns = 0.159154943091895335769L;
+    for (int i = 0; i < d / 2; ++i, ++pairs, turns *= ratio) {
       f.pair[pairs].turns = static_cast<uint64_t>(turns * 18446744073709551616.0L + 0.5L);
       f.pair[pairs].axis = a;
     }
@@ -464,8 +466,8 @@ qattn_status qattn_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, in
   DeviceInfo* d = nullptr;
   qattn_status st = device_info(&d);
   if (st != QATTN_OK) return st;
-  const qattn::GemmInt8Args a{M, N, K, 1, ldy, s_a_dev, s_b_dev, bias_dev, y, d->err, g_timeout_ns};
-  return from_cuda(qattn::launch_gemm_int8(a8, lda, b8, ldb, a, dtype == QATTN_DTYPE_FP16, d->num_sms, false,
+  const qattn::GemmInt8Args a{M, N, K, 1, 0, ldy, s_a_dev, s_b_dev, bias_dev, y, d->err, g_timeout_ns};
+  return from_cuda(qattn::launch_gemm_int8(a8, lda, b8, ldb, a, dtype == QATTN_DTYPE_FP16, d->num_sms,
                                            reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -480,12 +482,9 @@ qattn_status qattn_linear_int8(const void* x, int64_t ldx, qattn_dtype dtype, in
   DeviceInfo* d = nullptr;
   qattn_status st = device_info(&d);
   if (st != QATTN_OK) return st;
-  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const int fp16 = dtype == QATTN_DTYPE_FP16;
-  st = from_cuda(qattn::launch_quant_int8_rows(x, ldx, fp16, M, K, x8, ldx8, s_x_dev, d->err, cs));
-  if (st != QATTN_OK) return st;
-  const qattn::GemmInt8Args a{M, N, K, 1, ldy, s_x_dev, s_w_dev, bias_dev, y, d->err, g_timeout_ns};
-  return from_cuda(qattn::launch_gemm_int8(x8, ldx8, w8, ldw, a, fp16, d->num_sms, true, cs));
+  const qattn::GemmInt8Args a{M, N, K, 1, 0, ldy, s_x_dev, s_w_dev, bias_dev, y, d->err, g_timeout_ns};
+  return from_cuda(qattn::launch_linear_int8(x, ldx, x8, ldx8, s_x_dev, w8, ldw, a, dtype == QATTN_DTYPE_FP16,
+                                             d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 qattn_status qattn_forward(const uint8_t* q8, const uint8_t* k8, const uint8_t* v8,

@@ -128,13 +128,12 @@ __device__ __forceinline__ float2 ld_shared_f32x2(uint32_t addr) {
   return v;
 }
 
-// 16 bytes of the shared memory of any CTA of the cluster (address from mapa_shared, after the cluster barrier
-// that completes them: the address is formed behind it, so the load cannot move in front).
-__device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr) {
-  int4 v;
-  asm("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(cluster_addr));
-  return v;
+// 16 bytes into the shared memory of any CTA of the cluster, counted on an mbarrier of that CTA (both addresses
+// from mapa_shared).  Asynchronous: the CTA that stores need not wait for it.
+__device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, const int (&v)[4], uint32_t cluster_bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.s32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   cluster_addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(cluster_bar)
+               : "memory");
 }
 
 // Programmatic dependent launch: a kernel lets the next one of its stream start early, and that
@@ -202,6 +201,16 @@ __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
+}
+
+// The two halves of cluster_sync: every thread of a cluster does both, in this order.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Arrive on an mbarrier given by its cluster address (this CTA's or the peer's), with the
