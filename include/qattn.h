@@ -304,7 +304,7 @@ QATTN_API qattn_status qattn_norm_rope(const qattn_norm_rope_io* io, int n_io, i
  *   out[m, k] = rint(127 x[m, k] / amax_m), ties to even, of the exact quotient: -127 .. 127
  * x: device [M, K] bf16 or FP16, ldx elements between rows (any alignment; 16-byte aligned rows are
  * read faster).  out_int8: device [M, K] bytes, ldo between rows, 16-byte aligned, ldo % 16 == 0
- * (what lies between K and ldo is left as it was).  scale_dev: device [M].  A row with a
+ * (what lies between K and ldo is left as it was); it must not overlap x.  scale_dev: device [M].  A row with a
  * non-finite element gets scale NaN and codes 0 and records QATTN_ERR_NONFINITE; the other rows are
  * not affected. */
 QATTN_API qattn_status qattn_quantize_int8_rows(const void* x, int64_t ldx, qattn_dtype dtype, int M,
@@ -317,8 +317,9 @@ QATTN_API qattn_status qattn_quantize_int8_rows(const void* x, int64_t ldx, qatt
  * b8 [N, K]: device int8, lda / ldb bytes between rows (multiples of 16), 16-byte aligned.
  * y: device [M, N] bf16 or FP16, ldy elements between rows (16-byte aligned rows are written faster).
  * s_a_dev [M], s_b_dev [N], bias_dev [N] or NULL: device floats.  M, N, K >= 1 of any size,
- * K <= QATTN_INT8_MAX_K.  Few tokens (M <= 64) stream the weights once with K cut over clusters of CTAs, more
- * run on pairs of SMs; every path gives the same result.  An FP16 result past its range is infinite. */
+ * K <= QATTN_INT8_MAX_K.  One or two tokens, and up to 64, stream the weights once (the latter with K cut over
+ * clusters of CTAs), more run on pairs of SMs; every path gives the same result.  y must not overlap the inputs.  An
+ * FP16 result past its range is infinite. */
 QATTN_API qattn_status qattn_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb,
                                        void* y, int64_t ldy, qattn_dtype dtype, int M, int N, int K,
                                        const float* s_a_dev, const float* s_b_dev, const float* bias_dev,
@@ -326,7 +327,8 @@ QATTN_API qattn_status qattn_gemm_int8(const int8_t* a8, int64_t lda, const int8
 
 /* A linear layer on 16-bit activations: qattn_quantize_int8_rows of x into x8 and s_x_dev (caller-owned,
  * left filled), then qattn_gemm_int8 with them, the GEMM starting while the quantize runs (it loads weights
- * until the codes are there).  Same results and rules as the two calls. */
+ * until the codes are there; one launch for one or two tokens).  Same results and rules as the two calls: y may be x,
+ * and w8 and s_w may be x8 and s_x. */
 QATTN_API qattn_status qattn_linear_int8(const void* x, int64_t ldx, qattn_dtype dtype, int M, int N, int K,
                                          int8_t* x8, int64_t ldx8, float* s_x_dev, const int8_t* w8,
                                          int64_t ldw, const float* s_w_dev, const float* bias_dev, void* y,

@@ -141,6 +141,8 @@ class Int8Linear:
             raise ValueError(f"{M} tokens, made for {self.max_tokens}")
         if out is None:
             out = torch.empty(*shape[:-1], self.out_features, dtype=x.dtype, device=x.device)
+        if M == 0:
+            return out
         linear_int8(x, self._x8[:M], self._s_x[:M], self.w8, self.s_w, out.view(-1, self.out_features),
                     self.bias, stream)
         return out

@@ -91,6 +91,14 @@ qattn_status check_quant_rows(const void* x, int64_t ldx, qattn_dtype dtype, int
   return QATTN_OK;
 }
 
+// Whether two blocks of rows (`bytes` each, `stride` apart) may share memory.
+bool rows_overlap(const void* a, int64_t rows_a, int64_t stride_a, int64_t bytes_a, const void* b, int64_t rows_b,
+                  int64_t stride_b, int64_t bytes_b) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + static_cast<uintptr_t>((rows_b - 1) * stride_b + bytes_b) &&
+         b0 < a0 + static_cast<uintptr_t>((rows_a - 1) * stride_a + bytes_a);
+}
+
 qattn_status check_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb, const void* y,
                              int64_t ldy, qattn_dtype dtype, int M, int N, int K, const float* s_a,
                              const float* s_b, const float* bias) {
@@ -102,7 +110,7 @@ qattn_status check_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, in
     return QATTN_ERR_INVALID_ARG;
   // |sum| <= K * 2^14 has to fit int32; tile counts have to fit an int
   if (K > QATTN_INT8_MAX_K || lda > kMaxRowStride || ldb > kMaxRowStride) return QATTN_ERR_UNSUPPORTED;
-  if ((static_cast<int64_t>(M) / 256 + 1) * (static_cast<int64_t>(N) / 64 + 1) > (1 << 30))
+  if (M > (1 << 30) || N > (1 << 30) || (static_cast<int64_t>(M) / 256 + 1) * (static_cast<int64_t>(N) / 64 + 1) > (1 << 30))
     return QATTN_ERR_UNSUPPORTED;
   return QATTN_OK;
 }
@@ -483,8 +491,22 @@ qattn_status qattn_linear_int8(const void* x, int64_t ldx, qattn_dtype dtype, in
   qattn_status st = device_info(&d);
   if (st != QATTN_OK) return st;
   const qattn::GemmInt8Args a{M, N, K, 1, 0, ldy, s_x_dev, s_w_dev, bias_dev, y, d->err, g_timeout_ns};
-  return from_cuda(qattn::launch_linear_int8(x, ldx, x8, ldx8, s_x_dev, w8, ldw, a, dtype == QATTN_DTYPE_FP16,
-                                             d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int fp16 = dtype == QATTN_DTYPE_FP16;
+  // An output in the place of x, or weights, scales or a bias that are the quantize's own output, need the quantize to
+  // be done first: the two launches then follow each other.
+  const bool in_order = rows_overlap(y, M, 2 * ldy, 2 * int64_t{N}, x, M, 2 * ldx, 2 * int64_t{K}) ||
+                        rows_overlap(w8, N, ldw, K, x8, M, ldx8, K) || rows_overlap(w8, N, ldw, K, s_x_dev, 1, 0, 4 * int64_t{M}) ||
+                        rows_overlap(s_w_dev, 1, 0, 4 * int64_t{N}, s_x_dev, 1, 0, 4 * int64_t{M}) ||
+                        rows_overlap(s_w_dev, 1, 0, 4 * int64_t{N}, x8, M, ldx8, K) ||
+                        (bias_dev && (rows_overlap(bias_dev, 1, 0, 4 * int64_t{N}, s_x_dev, 1, 0, 4 * int64_t{M}) ||
+                                      rows_overlap(bias_dev, 1, 0, 4 * int64_t{N}, x8, M, ldx8, K)));
+  if (in_order) {
+    st = from_cuda(qattn::launch_quant_int8_rows(x, ldx, fp16, M, K, x8, ldx8, s_x_dev, d->err, cs));
+    if (st != QATTN_OK) return st;
+    return from_cuda(qattn::launch_gemm_int8(x8, ldx8, w8, ldw, a, fp16, d->num_sms, cs));
+  }
+  return from_cuda(qattn::launch_linear_int8(x, ldx, x8, ldx8, s_x_dev, w8, ldw, a, fp16, d->num_sms, cs));
 }
 
 qattn_status qattn_forward(const uint8_t* q8, const uint8_t* k8, const uint8_t* v8,

@@ -184,7 +184,8 @@ def test_offsets_past_32_bits():
     assert np.array_equal(w8.cpu().numpy(), want) and np.array_equal(s.cpu().numpy(), scale)
 
 
-@pytest.mark.parametrize("M,N,K,dtype", [(1, 96, 200, torch.bfloat16), (20, 515, 1003, torch.float16), (300, 260, 512, torch.bfloat16)])
+@pytest.mark.parametrize("M,N,K,dtype", [(1, 96, 200, torch.bfloat16), (2, 5001, 1003, torch.float16), (1, 40, 100000, torch.bfloat16),
+                                         (2, 300, 4096, torch.bfloat16), (20, 515, 1003, torch.float16), (300, 260, 512, torch.bfloat16)])
 def test_linear_is_its_two_calls(M, N, K, dtype):
     g = torch.Generator().manual_seed(M)
     x = torch.randn(M, K, generator=g).to(dtype).cuda()
@@ -198,6 +199,8 @@ def test_linear_is_its_two_calls(M, N, K, dtype):
     got = layer(x)
     assert qa.get_error() == 0
     assert torch.equal(got, y)
+    assert torch.equal(layer._x8[:M], x8) and torch.equal(layer._s_x[:M], s)
+    assert layer(x[:0]).shape == (0, N)
     xc, xs = oracle.quantize_int8_rows(x.double().cpu().numpy())
     wc, ws = oracle.quantize_int8_rows(w.double().cpu().numpy())
     assert np.array_equal(x8.cpu().numpy(), xc) and np.array_equal(layer.w8.cpu().numpy(), wc)
@@ -205,6 +208,53 @@ def test_linear_is_its_two_calls(M, N, K, dtype):
     assert torch.equal(layer(x.view(1, M, K)), y.view(1, M, N))
     with pytest.raises(ValueError):
         layer(torch.zeros(513, K, dtype=dtype, device="cuda"))
+
+
+@pytest.mark.parametrize("M", [1, 2, 40, 200])
+def test_linear_in_the_place_of_its_input_and_with_its_own_codes(M):
+    """y = x, and the product of the tokens' codes with themselves."""
+    K = 768
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).cuda()
+    layer = qa.Int8Linear((torch.randn(K, K, generator=g) * K ** -0.5).to(torch.bfloat16).cuda())
+    want = layer(x)
+    for _ in range(20):
+        y = x.clone()
+        assert layer(y, out=y).data_ptr() == y.data_ptr()
+        assert torch.equal(y, want)
+    x8, s = _padded(M, K)[1], torch.zeros(M, device="cuda")
+    gram = torch.empty(M, M, dtype=torch.bfloat16, device="cuda")
+    for i in range(5):
+        qa.linear_int8(x * (i + 1), x8, s, x8, s, gram)
+        codes, scale = oracle.quantize_int8_rows((x * (i + 1)).double().cpu().numpy())
+        _check(gram, codes, codes, scale, scale, None)
+    assert qa.get_error() == 0
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing of the set-up needs a call outside the capture (buffers and codes exist)."""
+    code = ("import torch, precision_quantized_attention_b200 as qa\n"
+            "x = torch.randn(1, 5, 2, 64, device='cuda').to(torch.bfloat16); w = torch.ones(64, device='cuda')\n"
+            "o = torch.zeros(1, 2, 5, 64, dtype=torch.bfloat16, device='cuda'); t = torch.zeros(5, 32, 2, device='cuda')\n"
+            "p = torch.arange(5, dtype=torch.int32, device='cuda')[:, None]\n"
+            "rows = [torch.randn(m, 1024, device='cuda').to(torch.bfloat16) for m in (1, 20, 200)]\n"
+            "w8 = torch.ones(256, 1024, dtype=torch.int8, device='cuda'); sw = torch.ones(256, device='cuda')\n"
+            "x8 = [torch.zeros(r.shape[0], 1024, dtype=torch.int8, device='cuda') for r in rows]\n"
+            "sx = [torch.zeros(r.shape[0], device='cuda') for r in rows]\n"
+            "y = [torch.zeros(r.shape[0], 256, dtype=torch.bfloat16, device='cuda') for r in rows]\n"
+            "torch.cuda.synchronize()\n"
+            "def step():\n"
+            "    qa.rope_table(p, (64,), t); qa.norm_rope([qa.NormRopeSegment(x, o, weight=w, table=t)])\n"
+            "    for r, a, s, b in zip(rows, x8, sx, y): qa.linear_int8(r, a, s, w8, sw, b)\n"
+            "g = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(g): step()\n"
+            "g.replay(); torch.cuda.synchronize()\n"
+            "got = [o.clone()] + [b.clone() for b in y]\n"
+            "step(); assert qa.get_error() == 0\n"
+            "assert all(torch.equal(a, b) for a, b in zip(got, [o] + y)) and o.abs().sum() > 0 and y[2].abs().sum() > 0\n"
+            "print('captured')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, (r.stdout + r.stderr)[-3000:]
 
 
 def test_linear_nonfinite_token_gives_nan_in_its_row_only():

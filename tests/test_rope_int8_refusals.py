@@ -84,7 +84,8 @@ def test_quantize_int8_rows_abi(kw, status):
     ({"bias": ctypes.c_void_p(0x10002)}, INVALID), ({"M": 0}, INVALID), ({"N": 0}, INVALID), ({"K": 0}, INVALID),
     ({"lda": 100}, INVALID), ({"lda": 96}, INVALID), ({"ldb": 104}, INVALID), ({"ldy": 6}, INVALID),
     ({"dtype": -1}, INVALID), ({"K": 131072, "lda": 131072, "ldb": 131072}, UNSUPPORTED),
-    ({"lda": 1 << 41}, UNSUPPORTED), ({"M": 1 << 30, "N": 1 << 20, "ldy": 1 << 20}, UNSUPPORTED)])
+    ({"lda": 1 << 41}, UNSUPPORTED), ({"M": 1 << 30, "N": 1 << 20, "ldy": 1 << 20}, UNSUPPORTED),
+    ({"N": (1 << 30) + 1, "ldy": 1 << 31}, UNSUPPORTED)])
 def test_gemm_int8_abi(kw, status):
     ok = (FAKE, 112, FAKE, 112, FAKE, 7, 0, 4, 7, 100, FAKE, FAKE, None)
     a = _with(GEMM, ok, kw)
