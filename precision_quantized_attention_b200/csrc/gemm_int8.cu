@@ -27,6 +27,16 @@ __device__ __forceinline__ uint16_t to16(float v) {
   if (FP16) return __half_as_ushort(__float2half_rn(v));
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
+// Two at once: one conversion instruction for both, on another unit than the single one's.
+template <bool FP16>
+__device__ __forceinline__ uint32_t to16x2(float lo, float hi) {
+  if (FP16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
 template <bool FP16>
 __device__ __forceinline__ float from16(uint32_t bits) {
   if (FP16) return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
@@ -658,28 +668,29 @@ struct Smem {
 
 // 32 x 32 outputs of a warp (lane = row m of the accumulator, columns n ..): y = acc * s_a * s_b + bias, through
 // shared memory so that a store instruction writes whole rows: 8 rows of 64 bytes where rows start on 16 bytes, else
-// one row's 32 neighbours.  Stored by the lanes as they hold the rows, an instruction touches 32 lines (the epilogue
-// then took twice the time, and at an odd N 4.5 times).  sb, bias: the 32 columns' values in shared memory.
+// one row's 32 neighbours.  Stored by the lanes as they hold the rows, an instruction touches 32 lines: a tile's
+// epilogue took 11000 clocks on four warps, 4400 now on eight.  sb, bias: the 32 columns' values in shared memory.
 template <bool FP16>
 __device__ __forceinline__ void epilogue_int8(const GemmInt8Args& a, const uint32_t (&v)[32], float s_m, int m_warp,
                                               int n, bool vec, const float* sb, const float* bias, uint8_t* tile) {
   if (!QATTN_IN_BOUNDS(a.err, n < a.N)) return;
   const int lane = threadIdx.x & 31;
   const int rows = min(32, a.M - m_warp);          // may be <= 0
+  const f32x2 s2 = pack_f32x2(s_m, s_m);
   // 16-byte piece j of row r lies at piece j ^ (r / 2 % 4): no bank conflict either way
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float4 s0 = *reinterpret_cast<const float4*>(sb + 8 * j), s1 = *reinterpret_cast<const float4*>(sb + 8 * j + 4);
-    const float4 b0 = *reinterpret_cast<const float4*>(bias + 8 * j), b1 = *reinterpret_cast<const float4*>(bias + 8 * j + 4);
-    const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-    const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+    const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(sb + 8 * j), s1 = *reinterpret_cast<const ulonglong2*>(sb + 8 * j + 4);
+    const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(bias + 8 * j), b1 = *reinterpret_cast<const ulonglong2*>(bias + 8 * j + 4);
+    const f32x2 sv[4] = {s0.x, s0.y, s1.x, s1.y}, bv[4] = {b0.x, b0.y, b1.x, b1.y};
     uint32_t p[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 8 * j + 2 * e;
-      const float lo = fmaf(static_cast<float>(static_cast<int>(v[i])) * s_m, sv[2 * e], bv[2 * e]);
-      const float hi = fmaf(static_cast<float>(static_cast<int>(v[i + 1])) * s_m, sv[2 * e + 1], bv[2 * e + 1]);
-      p[e] = static_cast<uint32_t>(to16<FP16>(lo)) | (static_cast<uint32_t>(to16<FP16>(hi)) << 16);
+      const f32x2 acc = pack_f32x2(static_cast<float>(static_cast<int>(v[i])), static_cast<float>(static_cast<int>(v[i + 1])));
+      float lo, hi;
+      unpack_f32x2(fma_f32x2(mul_f32x2(acc, s2), sv[e], bv[e]), lo, hi);
+      p[e] = to16x2<FP16>(lo, hi);
     }
     *reinterpret_cast<uint4*>(tile + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
   }
@@ -833,13 +844,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const uint32_t acc = tmem + lane_off + static_cast<uint32_t>(ab * BN + half * COLS);
-#pragma unroll 1
+      uint32_t v[2][32];
+      tmem_ld32(acc, v[0]);
+      tmem_wait_ld();
+#pragma unroll
       for (int c = 0; c < COLS; c += 32) {
         if (n0 + c >= args.N) break;               // uniform
-        uint32_t v[32];
-        tmem_ld32(acc + c, v);
+        // the next 32 columns are read while these are converted and stored
+        if (c + 32 < COLS) tmem_ld32(acc + c + 32, v[(c / 32 + 1) & 1]);
+        epilogue_int8<FP16>(args, v[(c / 32) & 1], s_m, m_warp, n0 + c, vec, sb + c, bias + c, stage);
         tmem_wait_ld();
-        epilogue_int8<FP16>(args, v, s_m, m_warp, n0 + c, vec, sb + c, bias + c, stage);
       }
       tc_fence_before();
       __syncwarp();
@@ -1030,14 +1044,14 @@ static cudaError_t launch_one_m(const OneArgs& o, const GemmInt8Args& a, int fp1
   return launch_one<2, QUANT>(o, a, fp16, num_sms, stream);
 }
 
-// Columns of a pair tile.  In us for a pair of SMs at 1.9 GHz: a K block of 128 takes 0.17, 0.19 and 0.26 for 64, 128
-// and 256 columns (the last bound by the MMA, the others by the copies), an epilogue that nothing overlaps 0.8,
-// 1.2 and 3.5; the pairs run waves of tiles.  Measured, 74 pairs, K = 4096 (64 / 128 / 256 columns): 200 x 4096
-// 11.0 / 12.1 / 16.7 us, 512 x 4096 16.5 / 12.5 / 17.0, 1024 x 4096 27.6 / 18.2 / 17.5, 2048 x 12288 128 / 256: 80.6 /
-// 70.6.
+// Columns of a pair tile.  The pairs run waves of tiles; a wave takes, in us for a K block of 128, 0.175, 0.195 and 0.30
+// with 64, 128 and 256 columns (the last at the MMA's rate, the others bound by the copies: 53 of 64 bytes a clock into
+// an SM), and the epilogue that nothing overlaps 0.5 and 1.6 more with 128 and 256 than with 64.  Measured on 74
+// pairs (64 / 128 / 256 columns), K = 4096: 100 x 4096 10.8 / 11.4 / 15.7 us, 512 x 4096 16.4 / 12.2 / 16.4, 1024 x 4096
+// 27.5 / 18.0 / 17.0, 1024 x 9216 49.6 / 32.5 / 28.6, 2048 x 12288 122 / 81.2 / 71.4; 700 x 7000 x 3000 26.6 / 20.6 / 22.2.
 static int pair_columns(int M, int N, int K, int pairs) {
   const int cols[3] = {64, 128, 256};
-  const double block[3] = {0.17, 0.19, 0.26}, tail[3] = {0.8, 1.2, 3.5};
+  const double block[3] = {0.175, 0.195, 0.30}, tail[3] = {0.0, 0.5, 1.6};
   const double kblocks = (K + pair8::BK - 1) / pair8::BK;
   int best = 256;
   double least = 1e30;

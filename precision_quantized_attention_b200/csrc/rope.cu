@@ -25,11 +25,12 @@ namespace qattn {
 // The nearest quarter turn and a rest of at most an eighth follow; cos and sin of the rest are FP32 sums, and rounding
 // the rest moves the angle by at most 2^-24 of pi / 4.  With the product and the reduction in FP64 (four operations and
 // a conversion a pair) the FP64 path bounded the kernel: 118800 tokens of 64 pairs took 21 us.
-// A block takes 32 tokens, or 128 where there are enough of them for every SM: their positions are split into words
+// A block takes 32 to 128 tokens, as many as fill whole rounds of resident blocks: their positions are split into words
 // once, then a thread keeps one pair, its frequency in registers, and steps over the tokens; a block's stores are
 // contiguous.
 // -------------------------------------------------------------------------------------------
 constexpr int TABLE_TOKENS = 128;
+constexpr int TABLE_BLOCKS = 6;                    // resident on an SM
 
 struct TablePos {
   uint32_t ip, fr;
@@ -49,7 +50,7 @@ __device__ __forceinline__ TablePos split_position(float p) {
 }
 
 template <class P, bool FRACTION>
-__global__ void __launch_bounds__(256) k_rope_table(const P* __restrict__ pos, int64_t pos_stride, int tokens,
+__global__ void __launch_bounds__(256, TABLE_BLOCKS) k_rope_table(const P* __restrict__ pos, int64_t pos_stride, int tokens,
                                                     int per_block, int axes, const __grid_constant__ RopeFreqs f,
                                                     float2* __restrict__ table) {
   // block: x = pair, y = token within a pass (no division)
@@ -91,7 +92,10 @@ __global__ void __launch_bounds__(256) k_rope_table(const P* __restrict__ pos, i
 
 cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_stride, int tokens, int axes,
                               int pairs, const RopeFreqs& f, float* table, int num_sms, cudaStream_t stream) {
-  const int per_block = tokens >= num_sms * TABLE_TOKENS ? TABLE_TOKENS : 32;
+  const int64_t round = static_cast<int64_t>(num_sms) * TABLE_BLOCKS;
+  const int64_t rounds = (tokens - 1) / (round * TABLE_TOKENS) + 1;
+  int per_block = static_cast<int>((tokens - 1) / (round * rounds) + 1);
+  if (per_block < 32) per_block = 32;
   const unsigned grid = static_cast<unsigned>((tokens - 1) / per_block + 1);
   const dim3 block(static_cast<unsigned>(pairs), static_cast<unsigned>(256 / pairs));
   if (pos_is_float)
