@@ -5,9 +5,11 @@
 //   y[m, n] = (sum_k c[m, k] w8[n, k]) * s[m] * s_w[n] (+ bias[n])
 //
 //   k_quant_int8_rows  the per-row quantize, one read of x (a row stays in registers)
-//   k_gemm_int8_few    few tokens (one tile of them): weight rows are the MMA's M, tokens its N, K is
-//                      split over a cluster whose partial sums meet in shared memory
+//   k_gemm_int8_one    one or two tokens: dp4a on streamed weights, with the quantize inside
+//   k_gemm_int8_few    up to 64 tokens: weight rows are the MMA's M, tokens its N, K is split over a cluster
+//                      whose partial sums meet in shared memory
 //   k_gemm_int8_pair   otherwise: 256 x BN output tiles on pairs of SMs (cta_group::2)
+// The sums are exact, so every path gives the same bits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -212,9 +214,11 @@ cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, 
 // for the first weights sooner than a copy engine, tensor memory and a cluster that have to be set up first.  A warp takes
 // ROWS weight rows at a time over all of K, eight chunks of 512 bytes in flight; the tokens' codes
 // lie in shared memory.  One row where every row then has its warp (N <= 32 for each SM), else two, which halves the
-// reads of the codes: 4096 x 11008 10.7 / 11.9 us, 4096 x 4096 5.7 / 6.0, 6144 x 4096 7.9 / 7.3, 18944 x 4096 14.3 / 14.1.
-// (More tokens are faster with the cluster kernel: four at 6144 x 4096 13.3 against 11.4.)  QUANT: every block quantizes the tokens itself (a few KB, from L2) while its first weights are on
-// their way, and block 0 also writes the codes and scales out, so that a linear layer is one launch.
+// reads of the codes: N x K = 4096 x 11008 10.7 / 11.9 us, 4096 x 4096 5.7 / 6.0, 6144 x 4096 7.9 / 7.3, 18944 x 4096
+// 14.3 / 14.1.  (More tokens are faster with the cluster kernel: four at 6144 x 4096 11.4 against 13.3.)
+// QUANT: every block quantizes the tokens itself (a few KB, from L2) while its first weights are on their way, and
+// block 0 also writes the codes and scales out, so that a linear layer is one launch.
+// Bound by the weights' stream and what it takes to start it: 18944 x 4096 runs at 5.9 TB/s, 6144 x 4096 at 3.7 of 6.55.
 // -------------------------------------------------------------------------------------------
 namespace one {
 constexpr int THREADS = 512, WARPS = THREADS / 32, BLOCKS = 2;   // per SM
@@ -395,6 +399,8 @@ __global__ void __launch_bounds__(one::THREADS, one::BLOCKS)
 //               each with every other group of eight tokens
 // The producer and the issuer are picked with elect.sync: under `lane == 0` the compiler moves every operand of a
 // copy or MMA through a vote, and a K block took 600 clocks instead of 370 whatever its size.
+// Bound by latency: a call takes 4.7 us before any stream (8 x 512 x 1024), 24 x 4096 x 11008 14.1 us with the quantize,
+// 45 MB of weights of which are 6.9.
 // -------------------------------------------------------------------------------------------
 namespace few {
 constexpr int BN = 128;                  // weight rows per CTA
@@ -640,6 +646,10 @@ __global__ void __launch_bounds__(few::THREADS, 2)
 //                       each TMEM lane quarter, each with half of the columns
 // (The producer and the issuer are picked with elect.sync, see above: 470 clocks a K block instead of 684.)
 // Tiles are visited m-fastest.  Every wait is bounded and both CTAs reach both cluster barriers.
+// Bound by the MMA: a 256 x 256 x 128 block takes 520 clocks of the pair (512 at the nominal rate), 8704 x 12288 x 4096
+// 265 to 300 us by the card's power limit (2920 to 3300 TOP/s); one wave (512 x 9216 x 4096, 17.6 us) adds 1.2 us until
+// the first block, 2.3 of epilogue and 1 at the end.  Two producers, as above, changed nothing here (18.0 against 18.2,
+// and 1 to 4 % slower at 4608 x 4096 x 12288).
 // -------------------------------------------------------------------------------------------
 namespace pair8 {
 constexpr int BM = 256;
