@@ -129,7 +129,7 @@ class Int8Linear:
         self.w8 = torch.zeros(N, ld, dtype=torch.int8, device=dev)[:, :K]
         self.s_w = torch.empty(N, dtype=torch.float32, device=dev)
         quantize_int8_rows(weight, self.w8, self.s_w)
-        self.bias = None if bias is None else bias.to(torch.float32).contiguous()
+        self.bias = None if bias is None else bias.detach().to(torch.float32).contiguous()
         self._x8 = torch.empty(self.max_tokens, ld, dtype=torch.int8, device=dev)[:, :K]
         self._s_x = torch.empty(self.max_tokens, dtype=torch.float32, device=dev)
 

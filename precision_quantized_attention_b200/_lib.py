@@ -551,16 +551,19 @@ def linear_int8(x, x8, s_x, w8, s_w, y, bias=None, stream=None):
     N = w8.shape[0]
     if y.dtype is not x.dtype:
         raise ValueError("y must have x's type")
+    if x8.dtype is not _I8 or w8.dtype is not _I8:
+        raise ValueError(f"x8 and w8 must be int8, got {x8.dtype} and {w8.dtype}")
     ldx, ld8 = _rows(x, M, K, "x"), _rows(x8, M, K, "x8", 16)
     ldw, ldy = _rows(w8, N, K, "w8", 16), _rows(y, M, N, "y")
     index = x.get_device()
     if x8.get_device() != index or w8.get_device() != index or y.get_device() != index:
         _same_device(index, x8=x8, w8=w8, y=y)
     handle = _launch_stream(index, stream)
-    _check(load().qattn_linear_int8(x.data_ptr(), ldx, dtype, M, N, K, _codes(x8, "x8"), ld8,
-                                    _vector(s_x, M, index, "s_x"), _codes(w8, "w8"), ldw,
-                                    _vector(s_w, N, index, "s_w"), _vector(bias, N, index, "bias"),
-                                    y.data_ptr(), ldy, handle), "qattn_linear_int8")
+    status = (_lib or load()).qattn_linear_int8(
+        x.data_ptr(), ldx, dtype, M, N, K, x8.data_ptr(), ld8, _vector(s_x, M, index, "s_x"), w8.data_ptr(), ldw,
+        _vector(s_w, N, index, "s_w"), None if bias is None else _vector(bias, N, index, "bias"), y.data_ptr(), ldy, handle)
+    if status:
+        _check(status, "qattn_linear_int8")
 
 
 def _scales(s_q, s_k, s_v):

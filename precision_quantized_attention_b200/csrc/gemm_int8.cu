@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256) k_quant_int8_rows(const uint16_t* __restr
 #pragma unroll
     for (int i = 1; i < WARPS; ++i) mx = max(mx, part[sub * WARPS + i]);
   }
-  if (m >= M || !QATTN_IN_BOUNDS(err, m >= 0)) return;
+  if (m >= M) return;
   const RowScale rs = row_scale_of<FP16>(mx);
   if (tid == 0) {
     if (!rs.finite) atomicExch(err, DEV_ERR_NONFINITE);
@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(256) k_quant_int8_rows(const uint16_t* __restr
   }
   int8_t* orow = out + static_cast<int64_t>(m) * ldo;
   auto put = [&](const uint4& u, int at) {
+    if (!QATTN_IN_BOUNDS(err, at >= 0 && at < K)) return;
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     uint2 c = make_uint2(0u, 0u);
     if (rs.finite) c = codes8<FP16>(w, rs.code);

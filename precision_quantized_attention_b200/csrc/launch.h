@@ -73,7 +73,8 @@ struct RopeFreqs {
   RopePair pair[128];
 };
 cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_stride, int tokens, int axes,
-                              int pairs, const RopeFreqs& f, float* table, int num_sms, cudaStream_t stream);
+                              int pairs, const RopeFreqs& f, float* table, int* err, int num_sms,
+                              cudaStream_t stream);
 
 // One tensor of a norm + rotation launch (rope.cu); strides in elements, channels contiguous.
 struct NormRopeSeg {

@@ -390,7 +390,7 @@ qattn_status qattn_rope_table(const void* pos_dev, qattn_pos_type pos_type, int6
   qattn_status st = device_info(&d);
   if (st != QATTN_OK) return st;
   return from_cuda(qattn::launch_rope_table(pos_dev, pos_type == QATTN_POS_FLOAT32, pos_stride, tokens,
-                                            n_axes, pairs, f, table_dev, d->num_sms,
+                                            n_axes, pairs, f, table_dev, d->err, d->num_sms,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 

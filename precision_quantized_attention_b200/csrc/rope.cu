@@ -53,7 +53,7 @@ __device__ __forceinline__ TablePos split_position(float p) {
 template <class P, bool FRACTION>
 __global__ void __launch_bounds__(256, TABLE_BLOCKS) k_rope_table(const P* __restrict__ pos, int64_t pos_stride, int tokens,
                                                     int per_block, int axes, const __grid_constant__ RopeFreqs f,
-                                                    float2* __restrict__ table) {
+                                                    float2* __restrict__ table, int* __restrict__ err) {
   // block: x = pair, y = token within a pass (no division)
   __shared__ TablePos at[TABLE_TOKENS * 8];        // 8 = most axes
   const int pairs = blockDim.x, p = threadIdx.x;
@@ -87,12 +87,14 @@ __global__ void __launch_bounds__(256, TABLE_BLOCKS) k_rope_table(const P* __res
     // a quarter turn swaps them and negates the new cosine, half a turn negates both
     const uint32_t flip = (q & 2u) << 30;
     const float c1 = (q & 1u) ? -s : c, s1 = (q & 1u) ? c : s;
-    out[t * pairs] = make_float2(__uint_as_float(__float_as_uint(c1) ^ flip), __uint_as_float(__float_as_uint(s1) ^ flip));
+    if (QATTN_IN_BOUNDS(err, t0 + t < tokens && p < pairs))
+      out[t * pairs] = make_float2(__uint_as_float(__float_as_uint(c1) ^ flip), __uint_as_float(__float_as_uint(s1) ^ flip));
   }
 }
 
 cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_stride, int tokens, int axes,
-                              int pairs, const RopeFreqs& f, float* table, int num_sms, cudaStream_t stream) {
+                              int pairs, const RopeFreqs& f, float* table, int* err, int num_sms,
+                              cudaStream_t stream) {
   const int64_t round = static_cast<int64_t>(num_sms) * TABLE_BLOCKS;
   const int64_t rounds = (tokens - 1) / (round * TABLE_TOKENS) + 1;
   int per_block = static_cast<int>((tokens - 1) / (round * rounds) + 1);
@@ -101,10 +103,10 @@ cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_str
   const dim3 block(static_cast<unsigned>(pairs), static_cast<unsigned>(256 / pairs));
   if (pos_is_float)
     k_rope_table<float, true><<<grid, block, 0, stream>>>(static_cast<const float*>(pos), pos_stride, tokens, per_block,
-                                                    axes, f, reinterpret_cast<float2*>(table));
+                                                    axes, f, reinterpret_cast<float2*>(table), err);
   else
     k_rope_table<int, false><<<grid, block, 0, stream>>>(static_cast<const int*>(pos), pos_stride, tokens, per_block,
-                                                  axes, f, reinterpret_cast<float2*>(table));
+                                                  axes, f, reinterpret_cast<float2*>(table), err);
   return cudaGetLastError();
 }
 
@@ -392,7 +394,7 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
   for (int h0 = h_first; h0 < h_end; h0 += heads) {
     load_step();
     cp_async_wait<ROPE_DEPTH>();
-    const bool in = h0 + hsub < h_end;
+    const bool in = h0 + hsub < h_end && QATTN_IN_BOUNDS(args.err, t < sg.L && h0 + hsub < sg.H);
     const uint4 v0 = ld_shared_v4(slot), v1 = ld_shared_v4(slot + 512);
     slot = slot + ROPE_STEP_BYTES == ring_end ? ring : slot + ROPE_STEP_BYTES;
     uint32_t w[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
