@@ -216,7 +216,7 @@ cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, 
 // ROWS weight rows at a time over all of K, eight chunks of 512 bytes in flight; the tokens' codes
 // lie in shared memory.  One row where every row then has its warp (N <= 32 for each SM), else two, which halves the
 // reads of the codes: N x K = 4096 x 11008 10.7 / 11.9 us, 4096 x 4096 5.7 / 6.0, 6144 x 4096 7.9 / 7.3, 18944 x 4096
-// 14.3 / 14.1.  (More tokens are faster with the cluster kernel: four at 6144 x 4096 11.4 against 13.3.)
+// 14.3 / 14.1.  (More tokens are faster with the cluster kernel: four at 6144 x 4096 10.5 against 13.3.)
 // QUANT: every block quantizes the tokens itself (a few KB, from L2) while its first weights are on their way, and
 // block 0 also writes the codes and scales out, so that a linear layer is one launch.
 // Bound by the weights' stream and what it takes to start it: 18944 x 4096 runs at 5.9 TB/s, 6144 x 4096 at 3.7 of 6.55.
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(one::THREADS, one::BLOCKS)
 
 // -------------------------------------------------------------------------------------------
 // Few tokens: bound by streaming the weights once.  One CTA takes 128 weight rows (the
-// MMA's M = 128, the TMEM lanes) against a tile of tokens (N = TOK, 16 to 64) over a range of K; the
+// MMA's M = 128, the TMEM lanes) against all tokens (N = TOK, 16 to 64) over a range of K; the
 // CTAs of a cluster share the 128 rows and cut K, so that a narrow layer still keeps every SM
 // loading.  int32 partial sums meet in distributed shared memory: exact, so neither the cut nor
 // the order changes a result, and no workspace or atomics are needed.  Groups of four tokens go round the CTAs; every
@@ -400,8 +400,9 @@ __global__ void __launch_bounds__(one::THREADS, one::BLOCKS)
 //               each with every other group of eight tokens
 // The producer and the issuer are picked with elect.sync: under `lane == 0` the compiler moves every operand of a
 // copy or MMA through a vote, and a K block took 600 clocks instead of 370 whatever its size.
-// Bound by latency: a call takes 4.7 us before any stream (8 x 512 x 1024), 24 x 4096 x 11008 14.1 us with the quantize,
-// 45 MB of weights of which are 6.9.
+// Bound by latency: a call takes 4 us before any stream (16 x 512 x 1024), 24 x 4096 x 11008 13.6 us with the quantize,
+// 45 MB of weights of which are 6.9.  (Up to 64 tokens: 64 x 4096 x 11008 12.8 us here and 19.4 on pairs of SMs, 64 x 9216
+// x 4096 12.1 / 16.3.)
 // -------------------------------------------------------------------------------------------
 namespace few {
 constexpr int BN = 128;                  // weight rows per CTA
@@ -428,7 +429,7 @@ struct Smem {
   static constexpr int ALONE = (226 * 1024 - OFF_STAGES - 1024) / STAGE < MOST_STAGES
                                    ? (226 * 1024 - OFF_STAGES - 1024) / STAGE : MOST_STAGES;
   static constexpr int SHARED = (112 * 1024 - OFF_STAGES - 1024) / STAGE;
-  static_assert(TILE_X % 1024 == 0 && SHARED >= 2, "alignment and stages");
+  static_assert(TILE_X % 1024 == 0 && SHARED >= 2 && NBARS <= 32, "alignment, stages, a lane for each barrier");
 };
 }  // namespace few
 
@@ -454,13 +455,11 @@ __global__ void __launch_bounds__(few::THREADS, 2)
   const int lane = threadIdx.x & 31;
   const int split = args.split;                           // CTAs of the cluster
   const int rank = static_cast<int>(cluster_ctarank());
-  const int tiles_n = (args.N + BN - 1) / BN;
-  const int tile = static_cast<int>(blockIdx.x) / split;
-  const int n0 = tile % tiles_n * BN, m0 = tile / tiles_n * TOK;
-  const int tokens = args.M - m0 < TOK ? args.M - m0 : TOK;
-  const int kblocks = (args.K + BK - 1) / BK;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / split);
-  const int nkb = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / split) - kb0;   // >= 1
+  const int n0 = static_cast<int>(cluster_id()) * BN;
+  // K blocks: each CTA kb_each, the first kb_more one more (no division here: with them, and the barriers set up by one
+  // thread, the first copy left 1 us later)
+  const int kb0 = rank * args.kb_each + (rank < args.kb_more ? rank : args.kb_more);
+  const int nkb = args.kb_each + (rank < args.kb_more ? 1 : 0);             // >= 1
 
   const uint32_t bar0 = base_u32 + S::OFF_BAR;
   auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -468,21 +467,20 @@ __global__ void __launch_bounds__(few::THREADS, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + S::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OFF_TMEM);
   float* s_tok = reinterpret_cast<float*>(base + S::OFF_SA);
-  const int groups = (tokens + 3) / 4, per = (groups - 1) / split + 1;      // of the tile; of an owner, at most
-  const int mine = (groups - rank + split - 1) / split;                     // of this CTA: rank, rank + split, ..
+  auto by_split = [&](int g) { return (g * args.split_inv) >> 16; };        // g / split for small g
+  const int tokens = args.M, groups = (tokens + 3) / 4, per = by_split(groups - 1) + 1;   // an owner's, at most
+  const int mine = by_split(groups - rank + split - 1);                     // this CTA's: rank, rank + split, ..
   const uint32_t stage0 = base_u32 + S::OFF_STAGES;
   const uint64_t tlim = args.timeout_ns;
   if (warp == 0) {
-    if (elect_one()) {
-      for (int i = 0; i < stages; ++i) { mbar_init(BAR(B_FULL + i), 1); mbar_init(BAR(B_EMPTY + i), 1); }
-      mbar_init(BAR(B_ACC), 1);
-      mbar_init(BAR(B_DRAIN), 1);
-      mbar_init(BAR(B_RED), 1);
-      *abort_flag = 0;
-      fence_mbar_init();
-      fence_proxy_async();
+    if (lane < S::NBARS) mbar_init(BAR(lane), 1);
+    if (lane == 0) *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
       if (split > 1 && mine > 0) mbar_arrive_expect_tx(BAR(B_RED), static_cast<uint32_t>(mine * split) * 2048u);
-      (void)QATTN_IN_BOUNDS(args.err, n0 < args.N && m0 < args.M && nkb >= 1 && kb0 + nkb <= kblocks);
+      (void)QATTN_IN_BOUNDS(args.err, n0 < args.N && nkb >= 1 && (kb0 + nkb - 1) * BK < args.K);
     }
     __syncwarp();
     asm volatile("bar.arrive 2, 352;" ::: "memory");   // the barriers are ready; nothing else is needed here
@@ -524,7 +522,7 @@ __global__ void __launch_bounds__(few::THREADS, 2)
       int u = 0;
       for (; u < nkb; ++u) {
         if (!mbar_wait(BAR(B_EMPTY + s), phase, tlim, abort_flag, args.err)) break;
-        tma_load_2d(stage0 + s * S::STAGE + TILE_W, &tm_x, BAR(B_FULL + s), (kb0 + u) * BK, m0);
+        tma_load_2d(stage0 + s * S::STAGE + TILE_W, &tm_x, BAR(B_FULL + s), (kb0 + u) * BK, 0);
         if (++s == stages) { s = 0; phase ^= 1u; }
       }
       // every copy has landed before the CTA may exit (instant when healthy)
@@ -567,10 +565,10 @@ __global__ void __launch_bounds__(few::THREADS, 2)
     // global memory they cost 128 round trips in a row (20 us).
     grid_wait_prior();
     for (int i = static_cast<int>(threadIdx.x) - 64; i < TOK; i += 256)
-      s_tok[i] = i < tokens ? row_scale(args, m0 + i) : 0.0f;
+      s_tok[i] = i < tokens ? row_scale(args, i) : 0.0f;
     asm volatile("bar.sync 1, 256;" ::: "memory");
     got = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_ACC), 0, tlim, abort_flag, args.err));
-    uint16_t* y = static_cast<uint16_t*>(args.y) + m0 * args.ldy + n;
+    uint16_t* y = static_cast<uint16_t*>(args.y) + n;
     // four tokens from column c on (their scales on 16 bytes)
     auto put4 = [&](const int (&a)[4], int c) {
       const float4 st = *reinterpret_cast<const float4*>(s_tok + c);
@@ -581,7 +579,7 @@ __global__ void __launch_bounds__(few::THREADS, 2)
       if (n < args.N) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (c + e < tokens && QATTN_IN_BOUNDS(args.err, m0 + c + e < args.M)) y[(c + e) * args.ldy] = o[e];
+          if (c + e < tokens && QATTN_IN_BOUNDS(args.err, c + e < args.M)) y[(c + e) * args.ldy] = o[e];
       }
     };
     if (split > 1) cluster_wait();                 // the peers' barriers are ready
@@ -601,8 +599,8 @@ __global__ void __launch_bounds__(few::THREADS, 2)
           if (split == 1) {
             put4(a, c + 4 * j);
           } else if (g < groups) {
-            const int owner = g % split;
-            st_async_v4(mapa_shared(base_u32 + S::OFF_RED + static_cast<uint32_t>(((rank * per + g / split) * 128 + r) * 16),
+            const int i = by_split(g), owner = g - i * split;
+            st_async_v4(mapa_shared(base_u32 + S::OFF_RED + static_cast<uint32_t>(((rank * per + i) * 128 + r) * 16),
                                     static_cast<uint32_t>(owner)),
                         a, mapa_shared(BAR(B_RED), static_cast<uint32_t>(owner)));
           }
@@ -672,7 +670,7 @@ struct Smem {
   static constexpr int ALLOC = OFF_T + EPI_WARPS * WARP_T + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   static constexpr uint32_t STAGE_TX = 2u * (TILE_A + TILE_B);
-  static_assert(TILE_B % 1024 == 0, "alignment");
+  static_assert(TILE_B % 1024 == 0 && NBARS <= 32, "alignment, a lane for each barrier");
   static_assert(ALLOC <= 227 * 1024, "shared memory per CTA");
 };
 }  // namespace pair8
@@ -751,11 +749,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
   constexpr int B_DRAIN = B_ACCE + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + S::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + S::OFF_TMEM);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) { mbar_init(BAR(B_FULL + i), 1); mbar_init(BAR(B_EMPTY + i), 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(BAR(B_ACCF + b), 1); mbar_init(BAR(B_ACCE + b), 2 * EPI_WARPS); }
-    mbar_init(BAR(B_DRAIN), 1);
-    *abort_flag = 0;
+  if (warp == 0) {                     // a lane for each barrier
+    if (lane < S::NBARS) mbar_init(BAR(lane), lane >= B_ACCE && lane < B_ACCE + 2 ? 2 * EPI_WARPS : 1);
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -953,15 +949,15 @@ static int few_resident(int split, int num_sms) {
   return n;
 }
 
-// CTAs that share 128 weight rows and a token tile: as many as keep all tiles resident at one CTA an SM, with at
-// least four K blocks each.  16 tokens, K = 4096, splits 1 / 2 / 3 / 4 / 8: N = 4096 9.9 / 9.0 / 8.5 / 8.1 / 8.6 us,
-// 6144 10.3 / 9.8 / 15.3 / 9.8 / 11.5, 1024 8.6 / 7.5 / 6.8 / 6.1 / 5.3, 12288 13.1 / 14.5 / 17.7 / 16.1 / 18.9.
+// CTAs that share 128 weight rows: as many as keep all tiles resident at one CTA an SM, with at least two K blocks
+// each.  16 tokens, K = 4096, splits 1 / 2 / 3 / 4 / 8: N = 4096 9.3 / 8.3 / 7.9 / 7.4 / 7.9 us, 6144 9.7 / 9.2 / 14.0 /
+// 9.5 / 10.9, 1024 7.8 / 6.7 / 6.1 / 5.4 / 4.5, 12288 12.4 / 13.7 / 16.0 / 15.0 / 17.1; 64 x 1024 x 1024 with four blocks
+// each 6.0, two 5.1.
 template <int TOK, bool FP16>
-static int few_split(int64_t tiles, int K, int num_sms) {
+static int few_split(int64_t tiles, int kblocks, int num_sms) {
   static DeviceOnce resident[9];
-  const int kblocks = (K + few::BK - 1) / few::BK;
   for (int split = 8; split > 1; --split) {
-    if (split > kblocks / 4 || tiles * split > num_sms) continue;
+    if (split > kblocks / 2 || tiles * split > num_sms) continue;
     if (tiles <= resident[split].get([split, num_sms] { return few_resident<TOK, FP16>(split, num_sms); })) return split;
   }
   return 1;
@@ -975,9 +971,13 @@ static cudaError_t launch_few(const int8_t* x, int64_t ldx, const int8_t* w, int
   CUtensorMap mw, mx;
   if (!make_map_rows(&mw, w, a.N, a.K, ldw, few::BN) || !make_map_rows(&mx, x, a.M, a.K, ldx, TOK))
     return cudaErrorInvalidValue;
-  const int64_t tiles = (static_cast<int64_t>(a.N) + few::BN - 1) / few::BN * ((a.M + TOK - 1) / TOK);
+  const int64_t tiles = (static_cast<int64_t>(a.N) + few::BN - 1) / few::BN;
+  const int kblocks = (a.K + few::BK - 1) / few::BK;
   GemmInt8Args b = a;
-  b.split = few_split<TOK, FP16>(tiles, a.K, num_sms);
+  b.split = few_split<TOK, FP16>(tiles, kblocks, num_sms);
+  b.split_inv = 65536 / b.split + 1;
+  b.kb_each = kblocks / b.split;
+  b.kb_more = kblocks % b.split;
   b.stages = tiles * b.split <= num_sms ? S::ALONE : S::SHARED;
   return launch_ex(k_gemm_int8_few<TOK, FP16>, once, dim3(static_cast<unsigned>(tiles * b.split)),
                    static_cast<unsigned>(b.split), few::THREADS, S::bytes(S::ALONE), S::bytes(b.stages), early, stream,

@@ -111,7 +111,9 @@ cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, 
                                    int64_t ldo, float* scale, int* err, cudaStream_t stream);
 struct GemmInt8Args {
   int M, N, K;
-  int split, stages;           // set by the launcher: CTAs that share a tile's K range, and their stages
+  // set by the launcher: CTAs that share a tile's K range, 65536 / split + 1, the K blocks of each and how many have one
+  // more, stages
+  int split, split_inv, kb_each, kb_more, stages;
   int64_t ldy;
   const float* s_a;
   const float* s_b;

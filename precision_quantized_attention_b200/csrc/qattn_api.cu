@@ -474,7 +474,7 @@ qattn_status qattn_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, in
   DeviceInfo* d = nullptr;
   qattn_status st = device_info(&d);
   if (st != QATTN_OK) return st;
-  const qattn::GemmInt8Args a{M, N, K, 1, 0, ldy, s_a_dev, s_b_dev, bias_dev, y, d->err, g_timeout_ns};
+  const qattn::GemmInt8Args a{M, N, K, 1, 0, 0, 0, 0, ldy, s_a_dev, s_b_dev, bias_dev, y, d->err, g_timeout_ns};
   return from_cuda(qattn::launch_gemm_int8(a8, lda, b8, ldb, a, dtype == QATTN_DTYPE_FP16, d->num_sms,
                                            reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -490,7 +490,7 @@ qattn_status qattn_linear_int8(const void* x, int64_t ldx, qattn_dtype dtype, in
   DeviceInfo* d = nullptr;
   qattn_status st = device_info(&d);
   if (st != QATTN_OK) return st;
-  const qattn::GemmInt8Args a{M, N, K, 1, 0, ldy, s_x_dev, s_w_dev, bias_dev, y, d->err, g_timeout_ns};
+  const qattn::GemmInt8Args a{M, N, K, 1, 0, 0, 0, 0, ldy, s_x_dev, s_w_dev, bias_dev, y, d->err, g_timeout_ns};
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int fp16 = dtype == QATTN_DTYPE_FP16;
   // An output in the place of x, or weights, scales or a bias that are the quantize's own output, need the quantize to

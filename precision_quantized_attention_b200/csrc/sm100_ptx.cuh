@@ -180,6 +180,13 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+// Index of the cluster in a one-dimensional grid.
+__device__ __forceinline__ uint32_t cluster_id() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+
 // One lane of the (converged) warp: true there, false in the others.
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
