@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(few::THREADS, 2)
 // (The producer and the issuer are picked with elect.sync, see above: 470 clocks a K block instead of 684.)
 // Tiles are visited m-fastest.  Every wait is bounded and both CTAs reach both cluster barriers.
 // Bound by the MMA: a 256 x 256 x 128 block takes 520 clocks of the pair (512 at the nominal rate), 8704 x 12288 x 4096
-// 265 to 300 us by the card's power limit (2920 to 3300 TOP/s); one wave (512 x 9216 x 4096, 17.6 us) adds 1.2 us until
+// 265 to 300 us by the card's power limit (2920 to 3300 TOP/s); one wave (512 x 9216 x 4096, 17.7 us) adds 1.2 us until
 // the first block, 2.3 of epilogue and 1 at the end.  Two producers, as above, changed nothing here (18.0 against 18.2,
 // and 1 to 4 % slower at 4608 x 4096 x 12288).
 // -------------------------------------------------------------------------------------------
@@ -666,9 +666,10 @@ struct Smem {
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBARS;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int OFF_T = (OFF_ABORT + 4 + 15) / 16 * 16; // per epilogue warp: 32 x 32 16-bit outputs,
-  static constexpr int WARP_T = 32 * 64 + 2 * (BN / 2) * 4;     // and its columns' scales and biases
+  static constexpr int COLS0 = (BN / 2 + 31) / 32 * 32;        // columns of the first epilogue warps; the others': the rest
+  static constexpr int WARP_T = 32 * 64 + 2 * COLS0 * 4;        // and its columns' scales and biases
   static constexpr int ALLOC = OFF_T + EPI_WARPS * WARP_T + 1024;
-  static constexpr uint32_t TMEM_COLS = 2 * BN;
+  static constexpr uint32_t TMEM_COLS = BN <= 64 ? 128 : BN <= 128 ? 256 : 512;
   static constexpr uint32_t STAGE_TX = 2u * (TILE_A + TILE_B);
   static_assert(TILE_B % 1024 == 0 && NBARS <= 32, "alignment, a lane for each barrier");
   static_assert(ALLOC <= 227 * 1024, "shared memory per CTA");
@@ -828,21 +829,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
   } else {
     // ======================= epilogue warps (both CTAs) =======================
     grid_wait_prior();                             // s_a comes from the preceding grid
-    constexpr int COLS = BN / 2;                   // of this warp
     const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int cols = half == 0 ? S::COLS0 : BN - S::COLS0;     // of this warp
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     uint8_t* stage = base + S::OFF_T + (warp - 2) * S::WARP_T;
     float* sb = reinterpret_cast<float*>(stage + 32 * 64);
-    float* bias = sb + COLS;
+    float* bias = sb + S::COLS0;
     const bool vec = (reinterpret_cast<uintptr_t>(args.y) & 15) == 0 && args.ldy % 8 == 0;
     int i = 0;
     for (int t = pair; t < tiles; t += npairs, ++i) {
       const int ab = i & 1;
       const int m_warp = (t % tiles_m) * BM + static_cast<int>(rank) * (BM / 2) + quarter * 32, m = m_warp + lane;
-      const int n0 = (t / tiles_m) * BN + half * COLS;
+      const int n0 = (t / tiles_m) * BN + half * S::COLS0;
       const float s_m = m < args.M ? row_scale(args, m) : 0.0f;
-#pragma unroll
-      for (int e = lane; e < COLS; e += 32) {
+      for (int e = lane; e < cols; e += 32) {
         sb[e] = n0 + e < args.N ? __ldg(args.s_b + n0 + e) : 0.0f;
         bias[e] = args.bias && n0 + e < args.N ? __ldg(args.bias + n0 + e) : 0.0f;
       }
@@ -850,15 +850,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair8::THREADS, 1)
       const bool ok = mbar_wait(BAR(B_ACCF + ab), (i >> 1) & 1, tlim, abort_flag, args.err);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + lane_off + static_cast<uint32_t>(ab * BN + half * COLS);
+      const uint32_t acc = tmem + lane_off + static_cast<uint32_t>(ab * BN + half * S::COLS0);
       uint32_t v[2][32];
       tmem_ld32(acc, v[0]);
       tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < COLS; c += 32) {
-        if (n0 + c >= args.N) break;               // uniform
+      for (int c = 0; c < S::COLS0; c += 32) {
+        if (c >= cols || n0 + c >= args.N) break;  // uniform
         // the next 32 columns are read while these are converted and stored
-        if (c + 32 < COLS) tmem_ld32(acc + c + 32, v[(c / 32 + 1) & 1]);
+        if (c + 32 < cols) tmem_ld32(acc + c + 32, v[(c / 32 + 1) & 1]);
         epilogue_int8<FP16>(args, v[(c / 32) & 1], s_m, m_warp, n0 + c, vec, sb + c, bias + c, stage);
         tmem_wait_ld();
       }
@@ -1055,18 +1055,19 @@ static cudaError_t launch_one_m(const OneArgs& o, const GemmInt8Args& a, int fp1
   return launch_one<2, QUANT>(o, a, fp16, num_sms, stream);
 }
 
-// Columns of a pair tile.  The pairs run waves of tiles; a wave takes, in us for a K block of 128, 0.175, 0.195 and 0.30
-// with 64, 128 and 256 columns (the last at the MMA's rate, the others bound by the copies: 53 of 64 bytes a clock into
-// an SM), and the epilogue that nothing overlaps 0.5 and 1.6 more with 128 and 256 than with 64.  Measured on 74
-// pairs (64 / 128 / 256 columns), K = 4096: 100 x 4096 10.8 / 11.4 / 15.7 us, 512 x 4096 16.4 / 12.2 / 16.4, 1024 x 4096
-// 27.5 / 18.0 / 17.0, 1024 x 9216 49.6 / 32.5 / 28.6, 2048 x 12288 122 / 81.2 / 71.4; 700 x 7000 x 3000 26.6 / 20.6 / 22.2.
+// Columns of a pair tile: the pairs run waves of tiles, and the width that fills its last wave best wins.  A wave takes,
+// in us for a K block of 128, 0.175 with 64 columns to 0.30 with 256 (the last at the MMA's rate, the narrow ones bound by
+// the copies: 53 of 64 bytes a clock into an SM), and the epilogue that nothing overlaps up to 1.6 more than with 64.
+// Measured on 74 pairs (64 / 128 / 160 / 192 / 224 / 256 columns): 333 x 5120 x 5120 25.7 / 20.0 / 14.5 / 16.2 / 17.1 /
+// 18.6 us, 1500 x 2048 x 8192 37.4 / 28.0 / 29.6 / 21.3 / 22.9 / 25.3, 512 x 4096 x 4096 16.3 / 12.0 / 12.8 / 14.2 / 15.1 / 16.3,
+// 1024 x 9216 x 4096 50.0 / 32.2 / 32.7 / 30.9 / 32.3 / 28.6, 2048 x 12288 x 4096 122 / 80.0 / 72.0 / 71.3 / 69.2 / 78.8.
 static int pair_columns(int M, int N, int K, int pairs) {
-  const int cols[3] = {64, 128, 256};
-  const double block[3] = {0.175, 0.195, 0.30}, tail[3] = {0.0, 0.5, 1.6};
+  const int cols[6] = {64, 128, 160, 192, 224, 256};
+  const double block[6] = {0.175, 0.195, 0.216, 0.232, 0.25, 0.30}, tail[6] = {0.0, 0.5, 0.8, 1.0, 1.3, 1.6};
   const double kblocks = (K + pair8::BK - 1) / pair8::BK;
   int best = 256;
   double least = 1e30;
-  for (int i = 2; i >= 0; --i) {
+  for (int i = 5; i >= 0; --i) {
     const int64_t tiles = (static_cast<int64_t>(M) + pair8::BM - 1) / pair8::BM * ((N + cols[i] - 1) / cols[i]);
     const double t = static_cast<double>((tiles + pairs - 1) / pairs) * kblocks * block[i] + tail[i];
     if (t < least) {
@@ -1083,10 +1084,14 @@ static cudaError_t launch_any(const int8_t* x, int64_t ldx, const int8_t* w, int
   if (a.M <= 16) return launch_few<16, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
   if (a.M <= 32) return launch_few<32, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
   if (a.M <= 64) return launch_few<64, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
-  const int cols = pair_columns(a.M, a.N, a.K, num_sms / 2);
-  if (cols == 64) return launch_pair<64, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
-  if (cols == 128) return launch_pair<128, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
-  return launch_pair<256, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+  switch (pair_columns(a.M, a.N, a.K, num_sms / 2)) {
+    case 64: return launch_pair<64, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+    case 128: return launch_pair<128, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+    case 160: return launch_pair<160, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+    case 192: return launch_pair<192, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+    case 224: return launch_pair<224, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+    default: return launch_pair<256, FP16>(x, ldx, w, ldw, a, num_sms, early, stream);
+  }
 }
 
 static cudaError_t launch_codes(const int8_t* a8, int64_t lda, const int8_t* b8, int64_t ldb, const GemmInt8Args& a,

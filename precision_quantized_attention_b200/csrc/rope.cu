@@ -192,19 +192,13 @@ __device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, const CodeD
   }
 }
 
-#ifndef QATTN_ROPE_WARPS
-#define QATTN_ROPE_WARPS 4
-#endif
-#ifndef QATTN_ROPE_BLOCKS
-#define QATTN_ROPE_BLOCKS 5
-#endif
-constexpr int ROPE_WARPS = QATTN_ROPE_WARPS;
+// Four warps a block and five blocks an SM (96 registers): 8704 tokens as E4M3 49 us then, with 8 warps x 2 or 3 blocks
+// 56 and 53, 6 blocks (spills) 51; two warps x 10 blocks the same.
+constexpr int ROPE_WARPS = 4, ROPE_BLOCKS = 5;
 // Steps whose loads are in flight: they go to shared memory (cp.async, each lane to its own words, so that no barrier
 // is needed), which leaves the registers to the arithmetic.
-#ifndef QATTN_ROPE_DEPTH
-#define QATTN_ROPE_DEPTH 3
-#endif
-constexpr int ROPE_DEPTH = QATTN_ROPE_DEPTH;
+// A depth of 3 and 4 measured the same, 5 and 8 slower.
+constexpr int ROPE_DEPTH = 3;
 constexpr int ROPE_STEP_BYTES = 32 * 2 * 16;       // a warp's step: two chunks a lane
 constexpr int ROPE_SMEM = ROPE_WARPS * (ROPE_DEPTH + 1) * ROPE_STEP_BYTES;
 
@@ -514,7 +508,7 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
 }
 
 template <int G, int MODE, bool FP16>
-__global__ void __launch_bounds__(32 * ROPE_WARPS, QATTN_ROPE_BLOCKS)
+__global__ void __launch_bounds__(32 * ROPE_WARPS, ROPE_BLOCKS)
     k_norm_rope(const __grid_constant__ NormRopeArgs args) {
   extern __shared__ __align__(128) uint8_t rope_ring[];
   int si = 0;

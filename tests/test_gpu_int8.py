@@ -139,8 +139,10 @@ def test_gemm_shapes(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(4, 128, 16384), (100, 384, 8192), (24, 4096, 1920), (1, 20000, 512),
-                                   (1200, 2100, 700), (640, 5000, 320), (1000, 4090, 4100)])
+                                   (1200, 2100, 700), (640, 5000, 320), (1000, 4090, 4100), (260, 5301, 1030),
+                                   (300, 6904, 1100), (520, 4700, 1200)])
 def test_gemm_larger(M, N, K):
+    """Long sums over clusters, and shapes that take tiles of 160, 128, 256, 160, 192 and 224 columns on 74 pairs."""
     ops = _operands(M, N, K, seed=K)
     _check(_gemm(*ops), *ops)
 
