@@ -248,6 +248,7 @@ typedef enum {
 #define QATTN_ROPE_MAX_DIM 256     /* channels of a head; rotated channels */
 #define QATTN_NORM_ROPE_MAX_IO 12  /* tensors of one qattn_norm_rope call */
 #define QATTN_INT8_MAX_K 131071    /* K * 2^14 fits int32 */
+/* Tokens, rows, heads and columns of the calls below: up to 2^30 each (QATTN_ERR_UNSUPPORTED past that). */
 
 /* Rotary table of tokens with several position axes (stream or frame, row, column): the token
  * positions that the transformer's Q and K rotation needs, made once for a resolution and kept.

@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr int kMaxRows = 1 << 30;       // rows, tokens, heads, columns: what the kernels round up stays an int
 constexpr int64_t kMaxRowStride = (int64_t{1} << 40) - 16;   // row stride of a TMA map, in bytes
 
 struct DeviceInfo {
@@ -87,7 +88,7 @@ qattn_status check_quant_rows(const void* x, int64_t ldx, qattn_dtype dtype, int
   if (!x || !out || !scale || M < 1 || K < 1 || ldx < K || ldo < K || ldo % 16 != 0) return QATTN_ERR_INVALID_ARG;
   if (dtype != QATTN_DTYPE_BF16 && dtype != QATTN_DTYPE_FP16) return QATTN_ERR_INVALID_ARG;
   if (!aligned(x, 2) || !aligned(out, 16) || !aligned(scale, 4)) return QATTN_ERR_INVALID_ARG;
-  if (ldo > kMaxRowStride || K > 0x7FF00000) return QATTN_ERR_UNSUPPORTED;
+  if (ldx > kMaxRowStride || ldo > kMaxRowStride || M > kMaxRows || K > kMaxRows) return QATTN_ERR_UNSUPPORTED;
   return QATTN_OK;
 }
 
@@ -109,8 +110,8 @@ qattn_status check_gemm_int8(const int8_t* a8, int64_t lda, const int8_t* b8, in
       (bias && !aligned(bias, 4)))
     return QATTN_ERR_INVALID_ARG;
   // |sum| <= K * 2^14 has to fit int32; tile counts have to fit an int
-  if (K > QATTN_INT8_MAX_K || lda > kMaxRowStride || ldb > kMaxRowStride) return QATTN_ERR_UNSUPPORTED;
-  if (M > (1 << 30) || N > (1 << 30) || (static_cast<int64_t>(M) / 256 + 1) * (static_cast<int64_t>(N) / 64 + 1) > (1 << 30))
+  if (K > QATTN_INT8_MAX_K || lda > kMaxRowStride || ldb > kMaxRowStride || ldy > kMaxRowStride) return QATTN_ERR_UNSUPPORTED;
+  if (M > kMaxRows || N > kMaxRows || (static_cast<int64_t>(M) / 256 + 1) * (static_cast<int64_t>(N) / 64 + 1) > (1 << 30))
     return QATTN_ERR_UNSUPPORTED;
   return QATTN_OK;
 }
@@ -370,6 +371,7 @@ qattn_status qattn_rope_table(const void* pos_dev, qattn_pos_type pos_type, int6
   if (pos_type != QATTN_POS_INT32 && pos_type != QATTN_POS_FLOAT32) return QATTN_ERR_INVALID_ARG;
   if (n_axes < 1 || n_axes > QATTN_ROPE_MAX_AXES || pos_stride < n_axes) return QATTN_ERR_INVALID_ARG;
   if (!aligned(pos_dev, 4) || !aligned(table_dev, 16)) return QATTN_ERR_INVALID_ARG;
+  if (tokens > kMaxRows) return QATTN_ERR_UNSUPPORTED;
   qattn::RopeFreqs f;
   int pairs = 0;
   for (int a = 0; a < n_axes; ++a) {
@@ -408,6 +410,7 @@ qattn_status qattn_norm_rope(const qattn_norm_rope_io* io, int n_io, int B, int 
     const qattn_norm_rope_io& t = io[i];
     qattn::NormRopeSeg& s = a.seg[i];
     if (!t.x || !t.out || t.H < 1 || t.L < 1) return QATTN_ERR_INVALID_ARG;
+    if (t.H > kMaxRows || t.L > kMaxRows) return QATTN_ERR_UNSUPPORTED;
     if (!aligned(t.x, 16) || (t.weight && !aligned(t.weight, 16)) || (t.table && !aligned(t.table, 16)) ||
         (t.amax && !aligned(t.amax, 4)))
       return QATTN_ERR_INVALID_ARG;

@@ -24,7 +24,7 @@ def _with(names, ok, kw):
     ({"tokens": 0}, INVALID), ({"n": 0}, INVALID), ({"n": 9}, INVALID), ({"dims": (16, 55, 56)}, INVALID),
     ({"dims": (16, 0, 56)}, INVALID), ({"dims": (128, 128, 2)}, UNSUPPORTED), ({"dims": (258, 2, 2)}, INVALID),
     ({"theta": (1e4, 0.0, 1e4)}, INVALID), ({"theta": (1e4, float("nan"), 1e4)}, INVALID),
-    ({"theta": (float("inf"),) * 3}, INVALID), ({"theta": (1e4, 0.5, 1e4)}, INVALID)])
+    ({"tokens": (1 << 30) + 1}, UNSUPPORTED), ({"theta": (float("inf"),) * 3}, INVALID), ({"theta": (1e4, 0.5, 1e4)}, INVALID)])
 def test_rope_table_abi(kw, status):
     names = ("pos", "type", "stride", "tokens", "n", "dims", "theta", "table")
     a = _with(names, (FAKE, 0, 3, 16, 3, (16, 56, 56), (1e4,) * 3, FAKE), kw)
@@ -46,7 +46,8 @@ def _io(**kw):
 @pytest.mark.parametrize("io,kw,status", [
     ({"x": None}, {}, INVALID), ({"out": None}, {}, INVALID), ({"x": 0x10008}, {}, INVALID),
     ({"out": 0x10008}, {}, INVALID), ({"weight": 0x10004}, {}, INVALID), ({"table": 0x10008}, {}, INVALID),
-    ({"H": 0}, {}, INVALID), ({"L": 0}, {}, INVALID), ({"x_stride_t": 260}, {}, INVALID),
+    ({"H": 0}, {}, INVALID), ({"L": 0}, {}, INVALID), ({"L": 2 ** 31 - 1}, {}, UNSUPPORTED),
+    ({"H": 2 ** 31 - 1}, {}, UNSUPPORTED), ({"x_stride_t": 260}, {}, INVALID),
     ({"out_stride_h": 2044}, {}, INVALID), ({"out_stride_h": 0}, {}, INVALID), ({"out_stride_t": 0}, {}, INVALID),
     ({}, {"B": 2}, INVALID),                             # batch rows of the output share elements
     ({"table_stride_b": 2}, {}, INVALID), ({}, {"R": 0}, INVALID), ({}, {"R": 24}, INVALID),
@@ -72,7 +73,8 @@ GEMM = ("a8", "lda", "b8", "ldb", "y", "ldy", "dtype", "M", "N", "K", "s_a", "s_
     ({"x": None}, INVALID), ({"out": None}, INVALID), ({"scale": None}, INVALID), ({"x": ODD}, INVALID),
     ({"out": ctypes.c_void_p(0x10008)}, INVALID), ({"scale": ctypes.c_void_p(0x10002)}, INVALID), ({"M": 0}, INVALID),
     ({"K": 0}, INVALID), ({"ldx": 99}, INVALID), ({"ldo": 96}, INVALID), ({"ldo": 120}, INVALID),
-    ({"dtype": 3}, INVALID), ({"ldo": 1 << 41}, UNSUPPORTED)])
+    ({"dtype": 3}, INVALID), ({"ldo": 1 << 41}, UNSUPPORTED), ({"M": 2 ** 31 - 1}, UNSUPPORTED),
+    ({"K": 2 ** 31 - 1, "ldx": 1 << 31, "ldo": 1 << 31}, UNSUPPORTED)])
 def test_quantize_int8_rows_abi(kw, status):
     a = _with(QUANT, (FAKE, 100, 0, 4, 100, FAKE, 112, FAKE), kw)
     assert _lib.load().qattn_quantize_int8_rows(*a, S0) == status
