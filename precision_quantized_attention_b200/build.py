@@ -31,7 +31,7 @@ def nvcc() -> str:
 def flags(verbose_ptxas: bool = False) -> list[str]:
     f = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE,
-         "--expt-relaxed-constexpr"]
+         "--expt-relaxed-constexpr", "--threads", "0"]
     if verbose_ptxas:
         f += ["-Xptxas", "-v"]
     return f
