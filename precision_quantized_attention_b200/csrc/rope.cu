@@ -494,11 +494,14 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
     } else {
       if (in && live0) *reinterpret_cast<uint4*>(out) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
       if (in && live1) *reinterpret_cast<uint4*>(out + second * 16) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
-      if (track) {                               // lanes and heads past the end hold zeros
+      if (track) {                               // what is stored: a group without a head or token may hold 0 * inf
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
+          if (in && (s == 0 ? live0 : live1)) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, w[s][i] & 0x7FFF7FFFu);
+            for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, w[s][i] & 0x7FFF7FFFu);
+          }
+        }
       }
     }
     out += o_step;

@@ -1,0 +1,44 @@
+"""Edges of rope_table and norm_rope: small sines, rows and groups without data, infinities next to
+channels that are not rotated, values near the type's largest, amax values that are no maximum.
+
+Bars (u = 2^-24).  A sine or cosine: the rest of the angle after whole quarter turns is rounded twice (2 u of
+itself) and resolved to 2^-53 quarter turns; its square, the sum's last steps, the first coefficient and the
+product add less than 4 u: 6 u of the value.  The angle: the frequency is held to 2^-65 turns and, as a power
+formed by up to 128 products in 64 bits, to 2^-57 of itself, the oracle's FP64 angle to 2^-51: together less than
+|a| 2^-50 + (|pos| + 6) 2^-62.  norm_rope: the bars of test_gpu_rope."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import precision_quantized_attention_b200 as qa
+from precision_quantized_attention_b200 import _lib
+from test_gpu_rope import check_codes
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+# whole numbers near multiples of pi: sines down to 1e-7
+NEAR_PI = [3, 22, 333, 355, 710, 103993, 104348, 208341, 312689, 833719, 1146408]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("B,L,H,D,R", [(1, 5, 3, 128, 128), (1, 1, 1, 64, 0), (2, 3, 5, 8, 0), (1, 7, 9, 24, 16),
+                                       (1, 2, 33, 256, 128), (1, 301, 2, 64, 64)])
+def test_running_amax_behind_a_norm_without_eps(B, L, H, D, R, inter, dtype):
+    """Lanes of a warp that hold no token, head or channel add nothing to the maximum, with eps = 0 too."""
+    g = torch.Generator().manual_seed(L * H + D)
+    x = (1 + torch.randn(B, L, H, D, generator=g).abs()).to(dtype).cuda()
+    w = (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    table = None
+    if R:
+        a = torch.rand(L, R // 2, generator=g) * 9
+        table = torch.stack([a.cos(), a.sin()], -1).cuda()
+    for eps in (0.0, 1e-6):
+        amax = torch.zeros(1, device="cuda")
+        out = torch.empty(B, H, L, D, dtype=dtype, device="cuda")
+        qa.norm_rope([qa.NormRopeSegment(x, out, weight=w, table=table, amax=amax)], eps=eps, interleaved=inter)
+        assert qa.get_error() == 0
+        assert amax.item() == out.abs().max().item()
