@@ -117,8 +117,10 @@ class Int8Linear:
     a scale for each output channel, x [M, K] in every call with a scale for each token.
 
     Holds the weight codes and the buffers of the activation codes for up to ``max_tokens`` rows, so that
-    calls allocate nothing but their result (give ``out`` to avoid that too).  Calls on one object
-    must not overlap on the device; stream order is enough.
+    calls allocate nothing but their result (give ``out`` to avoid that too) and a copy of an x whose
+    leading dimensions do not flatten to rows.  A call runs on ``stream`` (the current one if None), its
+    copy and its result's memory included; x has to be ready there, and the result is ready in that
+    stream's order.  Calls on one object must not overlap on the device; stream order is enough.
     """
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, max_tokens: int = 8704):
@@ -134,6 +136,21 @@ class Int8Linear:
         self._s_x = torch.empty(self.max_tokens, dtype=torch.float32, device=dev)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        if stream is None:
+            return self._run(x, out)
+        # what torch does around the call (the copy of an x whose rows are no view, the result's memory) belongs to
+        # the same stream; x and the result then live on two, and neither is freed into one while the other uses it
+        current = torch.cuda.current_stream(x.device)
+        if stream == current:
+            return self._run(x, out)
+        with torch.cuda.stream(stream):
+            y = self._run(x, out)
+        for t in (x, y):
+            t.record_stream(stream)
+            t.record_stream(current)
+        return y
+
+    def _run(self, x, out):
         shape = x.shape
         x = x.reshape(-1, shape[-1])
         M = x.shape[0]
@@ -144,5 +161,5 @@ class Int8Linear:
         if M == 0:
             return out
         linear_int8(x, self._x8[:M], self._s_x[:M], self.w8, self.s_w, out.view(-1, self.out_features),
-                    self.bias, stream)
+                    self.bias)
         return out
