@@ -255,7 +255,8 @@ typedef enum {
  *   pair i of axis a:  angle = pos[t, a] * theta[a]^(-2 i / axis_dims[a]),  i < axis_dims[a] / 2
  *   table[t, p] = (cos angle, sin angle) in FP32, p counting the pairs of axis 0 first, then axis 1 ...
  * pos_dev: device [tokens, n_axes] of pos_type, pos_stride elements (>= n_axes) between tokens;
- * fractional and negative positions are allowed.  The angle is formed and reduced in 64 bits.
+ * fractional and negative positions are allowed.  The angle is formed and reduced in 64 bits: it is off by at most
+ * (|pos| + 6) 2^-65 turns and 2^-56 of itself, and an entry by 6 x 2^-24 of its own value more, small sines included.
  * axis_dims (even) and theta (>= 1): HOST arrays of n_axes, read during the call.  table_dev: device
  * [tokens, R / 2, 2] floats with R = sum of axis_dims <= QATTN_ROPE_MAX_DIM, 16-byte aligned.
  * A non-finite position, or one past 2^31, gives NaN entries for its axis. */

@@ -11,6 +11,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "launch.h"
 #include "quant_math.cuh"
@@ -19,12 +20,13 @@
 namespace qattn {
 
 // -------------------------------------------------------------------------------------------
-// Rotary table.  The angle of a far position needs more than 32 bits before it is reduced.  It is formed in fixed
-// point, where the reduction to one turn is the overflow of the words: position ip + fr / 2^32 (32.32 bits) times the
-// pair's frequency in turns, 64 bits of fraction, gives the turn's 32 bits (2^-32 turns are 1.5e-9 rad).
-// The nearest quarter turn and a rest of at most an eighth follow; cos and sin of the rest are FP32 sums, and rounding
-// the rest moves the angle by at most 2^-24 of pi / 4.  (118800 tokens of 64 pairs: 13.8 us, 4.5 TB/s, bound by the
-// integer and FP32 instructions, 65 % of the issue slots; 4608 tokens 2.4 us, a launch.)  With the product and the reduction in FP64 (four operations and
+// Rotary table.  The angle of a far position needs more than 32 bits before it is reduced, and a small sine, of a small
+// angle or next to a multiple of pi, needs the bits behind the first 32 of its turn.  So the turn is held in 64 bits, in
+// fixed point, where the reduction to one turn is the overflow of the words: position (32.64 bits) times the pair's
+// frequency in turns, 64 bits of fraction.  The nearest quarter turn and a rest of at most an eighth follow; cos and sin of
+// the rest, rounded to 24 bits, are FP32 sums: 6 x 2^-24 of their value.  (With the turn cut off at 32 bits a sine near
+// 1e-6 was off by 6e-4 of itself.)  118800 tokens of 64 pairs: 13.9 us, 4.5 TB/s, bound by the integer and FP32
+// instructions; with fractional positions, whose products are two more, 17.5 us; 4608 tokens 2.4 us, a launch.  With the product and the reduction in FP64 (four operations and
 // a conversion a pair) the FP64 path bounded the kernel: 118800 tokens of 64 pairs took 21 us.
 // A block takes 32 to 128 tokens, as many as fill whole rounds of resident blocks: their positions are split into words
 // once, then a thread keeps one pair, its frequency in registers, and steps over the tokens; a block's stores are
@@ -33,63 +35,95 @@ namespace qattn {
 constexpr int TABLE_TOKENS = 128;
 constexpr int TABLE_BLOCKS = 6;                    // resident on an SM
 
-struct TablePos {
-  uint32_t ip, fr;
-  uint32_t neg;                                    // all ones for a negative ip
-  float nan;                                       // 0; NaN for a position that is not finite or past 2^31
+// A position as magnitude and sign: |position| = ip + (f_hi + f_lo / 2^32) / 2^32.
+struct alignas(16) TablePosInt {
+  uint32_t ip, sign;                               // sign: the sine's sign bit
+  float off;                                       // 2^-30; NaN for a position that is not finite or past 2^31
+};
+struct alignas(8) TablePosFloat {
+  uint32_t ip, sign;
+  float off;
+  uint32_t f_hi, f_lo;
 };
 
-__device__ __forceinline__ TablePos split_position(int v) {
-  return {static_cast<uint32_t>(v), 0u, v < 0 ? 0xFFFFFFFFu : 0u, 0.0f};
+__device__ __forceinline__ TablePosInt split_position(int v) {
+  const uint32_t u = static_cast<uint32_t>(v);
+  return {v < 0 ? 0u - u : u, u & 0x80000000u, 0x1p-30f};
 }
-__device__ __forceinline__ TablePos split_position(float p) {
-  const double v = static_cast<double>(p);
-  if (!(v >= -2147483648.0 && v < 2147483648.0)) return {0u, 0u, 0u, __int_as_float(0x7FFFFFFF)};
-  const double whole = floor(v);
-  return {static_cast<uint32_t>(static_cast<int>(whole)), __double2uint_rd((v - whole) * 4294967296.0),
-          whole < 0.0 ? 0xFFFFFFFFu : 0u, 0.0f};
+// Every step is exact: a float has 24 bits, so what is left of one below 1 or below 2^-32 is a float too.
+__device__ __forceinline__ TablePosFloat split_position(float v) {
+  if (!(v >= -2147483648.0f && v < 2147483648.0f)) return {0u, 0u, __int_as_float(0x7FFFFFFF), 0u, 0u};
+  const float m = fabsf(v);
+  const uint32_t ip = __float2uint_rz(m);
+  const float f = (m - static_cast<float>(ip)) * 4294967296.0f;
+  const uint32_t f_hi = __float2uint_rz(f);
+  return {ip, __float_as_uint(v) & 0x80000000u, 0x1p-30f, f_hi,
+          __float2uint_rz((f - static_cast<float>(f_hi)) * 4294967296.0f)};
 }
 
-template <class P, bool FRACTION>
+// What the fraction adds to the phase: the products' bits from 2^-64 on.
+__device__ __forceinline__ uint64_t fraction_phase(const TablePosInt&, uint32_t, uint32_t) { return 0; }
+__device__ __forceinline__ uint64_t fraction_phase(const TablePosFloat& v, uint32_t hi, uint32_t lo) {
+  return static_cast<uint64_t>(v.f_hi) * hi + __umulhi(v.f_hi, lo) + __umulhi(v.f_lo, hi);
+}
+__device__ __forceinline__ uint32_t has_fraction(const TablePosInt&) { return 0; }
+__device__ __forceinline__ uint32_t has_fraction(const TablePosFloat& v) { return v.f_hi | v.f_lo; }
+
+template <class P>
 __global__ void __launch_bounds__(256, TABLE_BLOCKS) k_rope_table(const P* __restrict__ pos, int64_t pos_stride, int tokens,
                                                     int per_block, int axes, const __grid_constant__ RopeFreqs f,
                                                     float2* __restrict__ table, int* __restrict__ err) {
   // block: x = pair, y = token within a pass (no division)
-  __shared__ TablePos at[TABLE_TOKENS * 8];        // 8 = most axes
+  using Pos = decltype(split_position(P()));
+  __shared__ Pos at[TABLE_TOKENS * 8];             // 8 = most axes
   const int pairs = blockDim.x, p = threadIdx.x;
   const int t0 = static_cast<int>(blockIdx.x) * per_block;
   const int n = min(per_block, tokens - t0);
+  uint32_t fraction = 0;
   for (int t = threadIdx.y * pairs + p; t < n; t += pairs * blockDim.y)
-    for (int a = 0; a < axes; ++a) at[t * 8 + a] = split_position(__ldg(pos + (t0 + t) * pos_stride + a));
-  __syncthreads();
+    for (int a = 0; a < axes; ++a) {
+      const Pos v = split_position(__ldg(pos + (t0 + t) * pos_stride + a));
+      fraction |= has_fraction(v);
+      at[t * 8 + a] = v;
+    }
+  if constexpr (std::is_same_v<P, float>) fraction = __syncthreads_or(static_cast<int>(fraction));
+  else __syncthreads();
   // Through a generic address: indexed by the thread, the constant bank serves one lane at a time (10 us of the 118800
   // tokens above).
   const RopeFreqs* freqs = &f;
   asm volatile("" : "+l"(freqs));
   const RopePair mine_f = freqs->pair[p];
   const uint32_t hi = static_cast<uint32_t>(mine_f.turns >> 32), lo = static_cast<uint32_t>(mine_f.turns);
-  const TablePos* mine = at + mine_f.axis;
+  const Pos* mine = at + mine_f.axis;
   float2* out = table + static_cast<int64_t>(t0) * pairs + p;
+  auto entries = [&](auto fractions) {
 #pragma unroll 4
-  for (int t = threadIdx.y; t < n; t += blockDim.y) {
-    const TablePos v = mine[t * 8];
-    // bits 32 to 63 of ip * (hi, lo), a negative ip having counted 2^32 too many, and of fr * hi / 2^32
-    uint32_t phase = v.ip * hi + __umulhi(v.ip, lo) - (lo & v.neg);
-    if (FRACTION) phase += __umulhi(v.fr, hi);
-    const uint32_t q = (phase + 0x20000000u) >> 30;          // nearest quarter turn
-    // Taylor sums of sin(pi x / 2) / x and cos(pi x / 2) in x^2 for the rest x, |x| <= 1/2 quarter turns:
-    // coefficients (pi / 2)^k / k!, the first ones left out below 2^-28
-    const float x = fmaf(static_cast<float>(static_cast<int>(phase - (q << 30))), 0x1p-30f, v.nan), z = x * x;
-    const float s =
-        x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 0.0001604411848f, -0.004681754135f), 0.07969262625f), -0.6459640975f), 1.570796327f);
-    const float c =
-        fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.520204237e-05f, 0.0009192602748f), -0.02086348076f), 0.2536695079f), -1.23370055f), 1.0f);
-    // a quarter turn swaps them and negates the new cosine, half a turn negates both
-    const uint32_t flip = (q & 2u) << 30;
-    const float c1 = (q & 1u) ? -s : c, s1 = (q & 1u) ? c : s;
-    if (QATTN_IN_BOUNDS(err, t0 + t < tokens && p < pairs))
-      out[t * pairs] = make_float2(__uint_as_float(__float_as_uint(c1) ^ flip), __uint_as_float(__float_as_uint(s1) ^ flip));
-  }
+    for (int t = threadIdx.y; t < n; t += blockDim.y) {
+      const Pos v = mine[t * 8];
+      uint64_t phase = mine_f.turns * v.ip;          // the turn's 64 bits
+      if constexpr (decltype(fractions)::value) phase += fraction_phase(v, hi, lo);
+      const uint32_t ph = static_cast<uint32_t>(phase >> 32);
+      const uint32_t q = (ph + 0x20000000u) >> 30;             // nearest quarter turn
+      // The rest x, |x| <= 1/2 quarter turns: its high word in units of 2^-30, and the low word's first 23 bits behind it
+      // (the mantissa of a float in [2^-30, 2^-29)), so that a small sine keeps 24 bits.  Then Taylor sums of
+      // sin(pi x / 2) / x and cos(pi x / 2) in x^2: coefficients (pi / 2)^k / k!, the first ones left out below 2^-28
+      const float low = __uint_as_float((static_cast<uint32_t>(phase) >> 9) + 0x30800000u) - v.off;
+      const float x = fmaf(static_cast<float>(static_cast<int>(ph - (q << 30))), 0x1p-30f, low), z = x * x;
+      const float s =
+          x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 0.0001604411848f, -0.004681754135f), 0.07969262625f), -0.6459640975f), 1.570796327f);
+      const float c =
+          fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.520204237e-05f, 0.0009192602748f), -0.02086348076f), 0.2536695079f), -1.23370055f), 1.0f);
+      // a quarter turn swaps them and negates the new cosine, half a turn negates both, a negative position the sine
+      const uint32_t flip = (q & 2u) << 30;
+      const float c1 = (q & 1u) ? -s : c, s1 = (q & 1u) ? c : s;
+      if (QATTN_IN_BOUNDS(err, t0 + t < tokens && p < pairs))
+        out[t * pairs] =
+            make_float2(__uint_as_float(__float_as_uint(c1) ^ flip), __uint_as_float(__float_as_uint(s1) ^ flip ^ v.sign));
+    }
+  };
+  // a block of whole numbers leaves the fractions' products out
+  if (fraction != 0) entries(std::true_type{});
+  else entries(std::false_type{});
 }
 
 cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_stride, int tokens, int axes,
@@ -102,10 +136,10 @@ cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_str
   const unsigned grid = static_cast<unsigned>((tokens - 1) / per_block + 1);
   const dim3 block(static_cast<unsigned>(pairs), static_cast<unsigned>(256 / pairs));
   if (pos_is_float)
-    k_rope_table<float, true><<<grid, block, 0, stream>>>(static_cast<const float*>(pos), pos_stride, tokens, per_block,
+    k_rope_table<float><<<grid, block, 0, stream>>>(static_cast<const float*>(pos), pos_stride, tokens, per_block,
                                                     axes, f, reinterpret_cast<float2*>(table), err);
   else
-    k_rope_table<int, false><<<grid, block, 0, stream>>>(static_cast<const int*>(pos), pos_stride, tokens, per_block,
+    k_rope_table<int><<<grid, block, 0, stream>>>(static_cast<const int*>(pos), pos_stride, tokens, per_block,
                                                   axes, f, reinterpret_cast<float2*>(table), err);
   return cudaGetLastError();
 }

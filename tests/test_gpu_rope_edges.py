@@ -4,7 +4,7 @@ channels that are not rotated, values near the type's largest, amax values that 
 Bars (u = 2^-24).  A sine or cosine: the rest of the angle after whole quarter turns is rounded twice (2 u of
 itself) and resolved to 2^-53 quarter turns; its square, the sum's last steps, the first coefficient and the
 product add less than 4 u: 6 u of the value.  The angle: the frequency is held to 2^-65 turns and, as a power
-formed by up to 128 products in 64 bits, to 2^-57 of itself, the oracle's FP64 angle to 2^-51: together less than
+formed by up to 128 products in 64 bits, to 2^-56 of itself, the oracle's FP64 angle to 2^-51: together less than
 |a| 2^-50 + (|pos| + 6) 2^-62.  norm_rope: the bars of test_gpu_rope."""
 import math
 
@@ -21,6 +21,31 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 # whole numbers near multiples of pi: sines down to 1e-7
 NEAR_PI = [3, 22, 333, 355, 710, 103993, 104348, 208341, 312689, 833719, 1146408]
+
+
+@pytest.mark.parametrize("kind", ["int", "whole", "fraction", "small"])
+@pytest.mark.parametrize("dims,theta", [((128,), 1e4), ((128,), 1e6), ((16, 56, 56), 1e4), ((2,), 10.0), ((256,), 1e10)])
+def test_small_sines_keep_their_relative_accuracy(dims, theta, kind):
+    n = len(dims)
+    if kind in ("int", "whole"):
+        p = np.array([s * v for v in list(range(100)) + NEAR_PI for s in (1, -1)], dtype=np.int64)
+        pos = torch.from_numpy(p).to(torch.int32 if kind == "int" else torch.float32)
+    elif kind == "fraction":                         # close to quarter turns, and anywhere
+        p = [s * k * math.pi / 2 for k in range(1, 200) for s in (1, -1)]
+        pos = torch.cat([torch.tensor(p), torch.randn(500, generator=torch.Generator().manual_seed(1)) * 30])
+    else:
+        pos = torch.randn(500, generator=torch.Generator().manual_seed(2)) * torch.logspace(-9, 0, 500)
+    pos = pos[:, None].expand(-1, n).contiguous()
+    table = torch.full((pos.shape[0], sum(dims) // 2, 2), 7.0, device="cuda")
+    qa.rope_table(pos.cuda(), dims, table, theta=theta)
+    assert qa.get_error() == 0
+    got = table.double().cpu().numpy()
+    a = oracle.rope_angles(pos.numpy(), dims, (theta,) * n)
+    size = np.abs(pos.double().numpy())[:, :1]
+    for i, want in ((0, np.cos(a)), (1, np.sin(a))):
+        tol = 6 * U * np.abs(want) + 2.0 ** -52 + np.abs(a) * 2.0 ** -50 + (size + 6) * 2.0 ** -62
+        off = np.abs(got[..., i] - want)
+        assert (off <= tol).all(), f"worst {np.max(off / tol):.2f} of the bar"
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
