@@ -67,3 +67,48 @@ def test_running_amax_behind_a_norm_without_eps(B, L, H, D, R, inter, dtype):
         qa.norm_rope([qa.NormRopeSegment(x, out, weight=w, table=table, amax=amax)], eps=eps, interleaved=inter)
         assert qa.get_error() == 0
         assert amax.item() == out.abs().max().item()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("D,R,inter", [(64, 32, True), (64, 32, False), (64, 48, False), (96, 64, True), (128, 0, True),
+                                       (128, 0, False), (184, 48, False), (256, 240, False)])
+def test_an_infinity_in_a_channel_that_is_not_rotated_stays_there(D, R, inter, weighted, dtype):
+    L, H = 6, 3
+    g = torch.Generator().manual_seed(D + R)
+    x = torch.randn(1, L, H, D, generator=g).to(dtype)
+    x[0, 1, 0, R + 2] = float("inf")
+    x[0, 2, 1, D - 1] = float("-inf")
+    x[0, 4, 2, R] = float("inf")
+    x[0, 4, 2, R + 1] = float("-inf")
+    if R:
+        x[0, 5, 0, 3] = float("inf")                 # a rotated one: its pair, and no other channel
+    w = (1 + 0.1 * torch.randn(D, generator=g)).cuda() if weighted else None
+    table = None
+    if R:
+        a = 0.3 + torch.rand(L, R // 2, generator=g)
+        table = torch.stack([a.cos(), a.sin()], -1).cuda()
+    elif not weighted:
+        return                                       # a copy
+    out = torch.empty(1, H, L, D, dtype=dtype, device="cuda")
+    codes = torch.empty(1, H, L, D, dtype=torch.uint8, device="cuda")
+    amax, scale = torch.full((1,), 3.0, device="cuda"), torch.zeros(1, device="cuda")
+    qa.norm_rope([qa.NormRopeSegment(x.cuda(), out, weight=w, table=table)], eps=1e-6, interleaved=inter)
+    assert qa.get_error() == _lib.ERR_NONFINITE
+    qa.norm_rope([qa.NormRopeSegment(x.cuda(), codes, weight=w, table=table, amax=amax, scale=scale)], eps=1e-6,
+                 interleaved=inter)
+    assert qa.get_error() == _lib.ERR_NONFINITE
+    host = lambda t: None if t is None else t.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want, size = oracle.norm_rope(host(x), host(w), host(table), 1e-6, inter)
+    got, got8 = host(out), codes.cpu().view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isnan(got8), np.isnan(want))
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf]) and np.array_equal(got8[inf], np.sign(want[inf]) * 448)
+    ok = np.isfinite(want)
+    half = torch.finfo(dtype).eps / 2
+    tol = 24 * U * size[ok] + half * (np.abs(want[ok]) + 24 * U * size[ok]) + 2.0 ** -25
+    assert (np.abs(got[ok] - want[ok]) <= tol).all()
+    s = float(scale.item())
+    value = lambda v: torch.from_numpy(np.clip(v / s, -448.0, 448.0)).float().to(torch.float8_e4m3fn).float().numpy()
+    assert (value(want[ok] - 28 * U * size[ok]) <= got8[ok]).all() and (got8[ok] <= value(want[ok] + 28 * U * size[ok])).all()
