@@ -152,7 +152,7 @@ cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_str
 //   y_j = r * (a_j x_j + b_j x_partner(j)),   a = w cos,   b = -/+ w_partner sin,
 // and reused for every head.  (A warp with more groups than the tensor has heads takes several tokens.)
 // Statistics, coefficients and products are 32-bit; y is rounded once, to the tensor's 16-bit type or, with
-// E4M3's 1 / scale in the coefficients, to its code.  Without norm and rotation (V) the codes are
+// E4M3's 1 / scale in r, to its code.  Without norm and rotation (V) the codes are
 // qattn_quantize_fp8's, the quotient correctly rounded.
 //
 // Bound by memory if the instructions fit: at 6.5 TB/s an SM has 23 ns, 170 issue slots, for 64 elements in and out as
@@ -271,18 +271,16 @@ struct Flag {
   static constexpr bool value = V;
 };
 
-// Coefficients of one chunk (channels c0 ..) of a token, times fold: the weight alone where nothing is rotated.  There b is
+// Coefficients of one chunk (channels c0 ..) of a token: the weight alone where nothing is rotated.  There b is
 // 0, unless the chunk's partner is then itself (SELF): a and b are half the weight, so that an infinity stays one and
 // is not multiplied with 0.
 template <int MODE, bool SELF>
 __device__ __forceinline__ void coefficients(const float* weight, const float* row, int c0, bool live, int R,
-                                             float fold, f32x2 (&ca)[4], f32x2 (&cb)[4]) {
+                                             f32x2 (&ca)[4], f32x2 (&cb)[4]) {
   float w[8], a[8], b[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] = 1.0f;
   if (weight != nullptr && live) load_f8(weight + c0, w);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] *= fold;
   if (row != nullptr && c0 < R) {                  // R is a multiple of 16: a chunk is in or out
     float cs[8];
     if (adjacent(MODE)) {
@@ -298,7 +296,7 @@ __device__ __forceinline__ void coefficients(const float* weight, const float* r
       const int half = R / 2;
       const bool upper = c0 >= half;
       const int other = upper ? c0 - half : c0 + half;
-      const float sign = upper ? fold : -fold;
+      const float sign = upper ? 1.0f : -1.0f;
       float wq[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) wq[j] = 1.0f;
@@ -381,8 +379,9 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
   for (int k = 0; k < ROPE_DEPTH; ++k) load_step();
 
   // E4M3: scale of the given amax (a non-finite amax writes no code).  Away from the ends of FP32 its
-  // reciprocal goes into the coefficients (PLAIN: into the correctly rounded quotient)
-  float fold = 1.0f;
+  // reciprocal goes into the norm's factor, behind the rotation: in the coefficients it could take products of large
+  // values past FP32's range that cancel (PLAIN: into the correctly rounded quotient)
+  float inv_s = 1.0f;
   CodeDiv cd{1.0f, true, 0, 0};
   if (E4M3) {
     const float amax = __ldg(sg.amax);
@@ -396,7 +395,7 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
     cd.rr = pack_f32x2(r, r);
     cd.ns = pack_f32x2(-cd.s, -cd.s);
     cd.fast = cd.s >= 0x1p-30f && cd.s <= 0x1p+30f;
-    if (!PLAIN && cd.fast) fold = r;
+    if (cd.fast) inv_s = r;
     if (first && lane == 0) *sg.scale_out = cd.s;
   }
 
@@ -406,8 +405,8 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
   bool src1[2] = {false, true};
   if (!PLAIN) {
     const float* row = sg.table == nullptr ? nullptr : sg.table + b * sg.table_b + static_cast<int64_t>(t) * args.R;
-    coefficients<MODE, MODE == ROT_LOW || MODE == ROT_SHUFFLE>(sg.weight, live0 ? row : nullptr, c0, live0, args.R, fold, ca[0], cb[0]);
-    coefficients<MODE, MODE == ROT_SHUFFLE>(sg.weight, live1 ? row : nullptr, c1, live1, args.R, fold, ca[1], cb[1]);
+    coefficients<MODE, MODE == ROT_LOW || MODE == ROT_SHUFFLE>(sg.weight, live0 ? row : nullptr, c0, live0, args.R, ca[0], cb[0]);
+    coefficients<MODE, MODE == ROT_SHUFFLE>(sg.weight, live1 ? row : nullptr, c1, live1, args.R, ca[1], cb[1]);
     if (MODE == ROT_SHUFFLE || MODE == ROT_LOW) {
       const int half8 = args.R / 16;               // chunks of half the rotated channels
 #pragma unroll
@@ -504,7 +503,8 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         bad32 = fmaf(ss, 0.0f, bad32);           // a non-finite element, or squares past FP32
-        const float r = rsqrtf(fmaf(ss, args.inv_d, args.eps));
+        float r = rsqrtf(fmaf(ss, args.inv_d, args.eps));
+        if (E4M3) r *= inv_s;
         const f32x2 r2 = pack_f32x2(r, r);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -514,7 +514,10 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) nan2 = note_nonfinite<FP16>(w[s][i], nan2);
+          for (int i = 0; i < 4; ++i) {
+            nan2 = note_nonfinite<FP16>(w[s][i], nan2);
+            if (E4M3) y[s][i] = mul_f32x2(y[s][i], pack_f32x2(inv_s, inv_s));
+          }
       }
       if (E4M3) {
 #pragma unroll

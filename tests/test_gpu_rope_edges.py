@@ -112,3 +112,20 @@ def test_an_infinity_in_a_channel_that_is_not_rotated_stays_there(D, R, inter, w
     s = float(scale.item())
     value = lambda v: torch.from_numpy(np.clip(v / s, -448.0, 448.0)).float().to(torch.float8_e4m3fn).float().numpy()
     assert (value(want[ok] - 28 * U * size[ok]) <= got8[ok]).all() and (got8[ok] <= value(want[ok] + 28 * U * size[ok])).all()
+
+
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("amax", [1e-5, 3.0, 1e30])
+def test_codes_of_a_rotation_of_values_near_the_largest(amax, inter):
+    """Products with 1 / scale would pass FP32's range and cancel to NaN; the rotated values do not."""
+    D, L, H = 64, 9, 2
+    g = torch.Generator().manual_seed(1)
+    x = (torch.rand(1, L, H, D, generator=g) * 1e38 + 2e38).to(torch.bfloat16).cuda()
+    a = math.pi / 4 + 0.01 * torch.randn(L, D // 2, generator=g)
+    table = torch.stack([a.cos(), a.sin()], -1).cuda()
+    codes = torch.empty(1, H, L, D, dtype=torch.uint8, device="cuda")
+    scale = torch.zeros(1, device="cuda")
+    qa.norm_rope([qa.NormRopeSegment(x, codes, table=table, amax=torch.full((1,), amax, device="cuda"), scale=scale)],
+                 interleaved=inter)
+    assert qa.get_error() == 0
+    check_codes(codes, float(scale.item()), x, None, table, 1e-6, inter)
