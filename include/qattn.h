@@ -295,7 +295,9 @@ typedef struct {
  * Heads may differ between tensors (grouped heads); L and H >= 1.  out must not overlap any x.
  * A non-finite element, or a row whose squares pass FP32, records QATTN_ERR_NONFINITE (its outputs
  * are what the arithmetic gives: NaN codes for NaN, +-448 for infinities); so does a non-finite given
- * amax, and that tensor's codes and scale are not written. */
+ * amax, and that tensor's codes and scale are not written.  The mean square is an FP32 number: with eps 0 a row of zeros
+ * gives NaN, as the formula does, and rows with no element above about 1e-19 (squares below FP32's normal range) lose
+ * accuracy or become infinite; these are not recorded. */
 QATTN_API qattn_status qattn_norm_rope(const qattn_norm_rope_io* io, int n_io, int B, int D,
                                        int rotary_dim, int interleaved, float eps, qattn_dtype dtype,
                                        qattn_stream_t stream);
