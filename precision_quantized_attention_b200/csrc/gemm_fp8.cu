@@ -81,7 +81,7 @@ __device__ __forceinline__ CodeScale code_scale(const GemmArgs& a) {
   CodeScale cs{1.0f, 1.0f, true, false};
   if (!a.codes) return cs;
   const float amax = __ldg(a.amax);
-  if (!(amax <= 3.402823466e38f)) {              // inf or NaN: no code is written
+  if (!(fabsf(amax) <= 3.402823466e38f)) {              // inf or NaN: no code is written
     if (blockIdx.x == 0 && threadIdx.x == 64) atomicExch(a.err, DEV_ERR_NONFINITE);
     return cs;
   }

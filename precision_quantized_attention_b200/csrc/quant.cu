@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256) k_quant_fp8(const uint4* __restrict__ xv,
                                                    float* __restrict__ scale_out,
                                                    int* __restrict__ err) {
   const float amax = *amax_p;
-  if (!(amax <= 3.402823466e38f)) {  // inf or NaN: nothing is written
+  if (!(fabsf(amax) <= 3.402823466e38f)) {  // inf or NaN: nothing is written
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(err, DEV_ERR_NONFINITE);
     return;
   }
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256) k_quant_fp4_block(
     float* __restrict__ gscale_out, uint4* __restrict__ codes8_out,
     float* __restrict__ scale8_out, int* __restrict__ err) {
   const float amax = *amax_p;
-  if (!(amax <= 3.402823466e38f)) {
+  if (!(fabsf(amax) <= 3.402823466e38f)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(err, DEV_ERR_NONFINITE);
     return;
   }
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(STATIC_THREADS) k_quant_qkv(const __grid_const
   const int ti = blockIdx.y;
   const QkvTensor tp = ti == 0 ? a.t[0] : (ti == 1 ? a.t[1] : a.t[2]);
   const float amax = *tp.amax;
-  if (!(amax <= 3.402823466e38f)) {              // inf or NaN: nothing is written
+  if (!(fabsf(amax) <= 3.402823466e38f)) {              // inf or NaN: nothing is written
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.err, DEV_ERR_NONFINITE);
     return;
   }

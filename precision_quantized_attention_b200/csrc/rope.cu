@@ -385,7 +385,7 @@ __device__ __forceinline__ uint32_t norm_rope_heads(const NormRopeArgs& args, co
   CodeDiv cd{1.0f, true, 0, 0};
   if (E4M3) {
     const float amax = __ldg(sg.amax);
-    if (!(amax <= 3.402823466e38f)) {              // inf or NaN
+    if (!(fabsf(amax) <= 3.402823466e38f)) {              // inf or NaN
       cp_async_wait<0>();
       bad = true;
       return 0;

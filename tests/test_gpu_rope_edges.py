@@ -129,3 +129,30 @@ def test_codes_of_a_rotation_of_values_near_the_largest(amax, inter):
                  interleaved=inter)
     assert qa.get_error() == 0
     check_codes(codes, float(scale.item()), x, None, table, 1e-6, inter)
+
+
+def test_a_given_amax_of_minus_infinity_writes_no_code():
+    x = torch.ones(1, 5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in (float("-inf"), float("inf"), float("nan")):
+        for w in (None, torch.ones(64, device="cuda")):
+            amax, scale = torch.full((1,), bad, device="cuda"), torch.full((1,), 5.0, device="cuda")
+            codes = torch.full((1, 2, 5, 64), 0x55, dtype=torch.uint8, device="cuda")
+            qa.norm_rope([qa.NormRopeSegment(x, codes, weight=w, amax=amax, scale=scale)])
+            assert qa.get_error() == _lib.ERR_NONFINITE
+            assert bool((codes == 0x55).all()) and scale.item() == 5.0
+        new = lambda n, v=0x55: torch.full((n,), v, dtype=torch.uint8, device="cuda")
+        codes, e2m1, block = new(640), new(320), new(40)
+        scale, scales = torch.full((1,), 5.0, device="cuda"), torch.full((3,), 5.0, device="cuda")
+        qa.quantize_fp8(x.view(-1), amax, codes, scale)
+        assert qa.get_error() == _lib.ERR_NONFINITE
+        qa.quantize_fp4_block(x.view(-1), amax, e2m1, block, scale)
+        assert qa.get_error() == _lib.ERR_NONFINITE
+        qa.quantize_qkv([x.view(-1)] * 3, amax.expand(3).contiguous(), [codes] * 3, scales)
+        assert qa.get_error() == _lib.ERR_NONFINITE
+        a8 = new(128 * 128, 0x30).view(128, 128)
+        one, product = torch.ones(1, device="cuda"), new(128 * 32).view(128, 32)
+        qa.gemm_fp8_e4m3(a8, a8[:32], product, one, one, amax, scale)
+        assert qa.get_error() == _lib.ERR_NONFINITE
+        for t in (codes, e2m1, block, product):
+            assert bool((t == 0x55).all())
+        assert scale.item() == 5.0 and bool((scales == 5.0).all())
