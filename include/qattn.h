@@ -291,7 +291,8 @@ typedef struct {
  * A tensor with neither weight nor table is copied (V).  E4M3: code = e4m3(y / s), s = fl32(amax / 448) of the
  * given amax, from the FP32 y, rounded once (a copied tensor gets exactly the codes of qattn_quantize_fp8).
  * Running amax: *amax = max(*amax, max |16-bit y|) (the caller clears it before the first call of a calibration; tensors that
- * share an amax are joined).  D % 8 == 0, D <= QATTN_ROPE_MAX_DIM; rotary_dim <= D, a multiple of 16.
+ * share an amax are joined).  A scale_out must not be an amax of the call, nor a running amax a given one, and tensors that
+ * share a scale_out share their amax.  D % 8 == 0, D <= QATTN_ROPE_MAX_DIM; rotary_dim <= D, a multiple of 16.
  * Heads may differ between tensors (grouped heads); L and H >= 1.  out must not overlap any x.
  * A non-finite element, or a row whose squares pass FP32, records QATTN_ERR_NONFINITE (its outputs
  * are what the arithmetic gives: NaN codes for NaN, +-448 for infinities); so does a non-finite given

@@ -442,6 +442,16 @@ qattn_status qattn_norm_rope(const qattn_norm_rope_io* io, int n_io, int B, int 
     s.L = t.L;
     s.e4m3 = t.out_e4m3 != 0;
   }
+  // No block may read as a given amax what another one writes (a scale, a running amax), nor two write different scales
+  // to one place.  Tensors that share a running amax, or a given one and its scale, are fine.
+  for (int i = 0; i < n_io; ++i) {
+    const qattn::NormRopeSeg& s = a.seg[i];
+    for (int j = 0; s.e4m3 && j < n_io; ++j) {
+      const qattn::NormRopeSeg& t = a.seg[j];
+      if (t.amax == s.scale_out || (!t.e4m3 && t.amax == s.amax)) return QATTN_ERR_INVALID_ARG;
+      if (t.e4m3 && t.scale_out == s.scale_out && t.amax != s.amax) return QATTN_ERR_INVALID_ARG;
+    }
+  }
   a.n = n_io;
   a.D = D;
   a.R = rotary_dim;
