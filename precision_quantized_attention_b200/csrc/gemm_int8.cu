@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(few::THREADS, 2)
         }
       }
       if (split > 1 && mine > 0) {
-        got = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(B_RED), 0, tlim, abort_flag, args.err));
+        got = __all_sync(0xFFFFFFFFu, mbar_wait<true>(BAR(B_RED), 0, tlim, abort_flag, args.err));   // the peers' stores
         for (int i = half; got && i < mine; i += 2) {
           int a[4] = {0, 0, 0, 0};
           for (int p = 0; p < split; ++p) {

@@ -76,15 +76,31 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same where the phase is completed by another CTA of the cluster whose stores (st_async_v4) are then read here
+// with plain loads: the default acquire orders them only against threads of this CTA.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait: spins on try_wait, reading the global timer every 256 failed polls.  Returns
 // false (and records DEV_ERR_TIMEOUT in *err) once `limit_ns` has passed, or immediately if
-// another role of the CTA already gave up (*abort != 0).  Never waits forever.
+// another role of the CTA already gave up (*abort != 0).  Never waits forever.  CLUSTER: mbar_try_wait_cluster.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           volatile int* abort, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
+  auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if ((it & 255u) == 0) {
       if (*abort) return false;
       if (global_timer_ns() - t0 > limit_ns) {
