@@ -606,8 +606,9 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, ROPE_BLOCKS)
       const float a = FP16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(mm)))
                            : __uint_as_float(mm << 16);
       if (mm >= (FP16 ? 0x7C00u : 0x7F80u)) atomicExch(args.err, DEV_ERR_NONFINITE);   // also by rounding
-      unsigned* dst = reinterpret_cast<unsigned*>(sg.amax);
-      if (__float_as_uint(a) > *static_cast<volatile unsigned*>(dst)) atomicMax(dst, __float_as_uint(a));
+      // a >= 0, so that bit patterns compare as signed integers, with a negative start (-infinity) below all of them
+      int* dst = reinterpret_cast<int*>(sg.amax);
+      if (__float_as_int(a) > *static_cast<volatile int*>(dst)) atomicMax(dst, __float_as_int(a));
     }
   }
 }

@@ -156,3 +156,14 @@ def test_a_given_amax_of_minus_infinity_writes_no_code():
         for t in (codes, e2m1, block, product):
             assert bool((t == 0x55).all())
         assert scale.item() == 5.0 and bool((scales == 5.0).all())
+
+
+@pytest.mark.parametrize("start", [float("-inf"), -1.0, -0.0, 0.5, 1e30])
+def test_running_amax_continues_from_any_number(start):
+    x = torch.randn(1, 7, 3, 64, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    for w in (None, torch.ones(64, device="cuda")):
+        out = torch.empty(1, 3, 7, 64, dtype=torch.bfloat16, device="cuda")
+        amax = torch.full((1,), start, device="cuda")
+        qa.norm_rope([qa.NormRopeSegment(x, out, weight=w, amax=amax)])
+        assert qa.get_error() == 0
+        assert amax.item() == max(np.float32(start), out.abs().max().item())
