@@ -219,7 +219,7 @@ cudaError_t launch_quant_int8_rows(const void* x, int64_t ldx, int fp16, int M, 
 // 14.3 / 14.1.  (More tokens are faster with the cluster kernel: four at 6144 x 4096 10.5 against 13.3.)
 // QUANT: every block quantizes the tokens itself (a few KB, from L2) while its first weights are on their way, and
 // block 0 also writes the codes and scales out, so that a linear layer is one launch.
-// Bound by the weights' stream and what it takes to start it: 18944 x 4096 runs at 5.9 TB/s, 6144 x 4096 at 3.7 of 6.55.
+// Bound by the weights' stream and what it takes to start it: 18944 x 4096 runs at 5.5 TB/s, 6144 x 4096 at 3.7 of 6.55.
 // -------------------------------------------------------------------------------------------
 namespace one {
 constexpr int THREADS = 512, WARPS = THREADS / 32, BLOCKS = 2;   // per SM
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(one::THREADS, one::BLOCKS)
 //               each with every other group of eight tokens
 // The producer and the issuer are picked with elect.sync: under `lane == 0` the compiler moves every operand of a
 // copy or MMA through a vote, and a K block took 600 clocks instead of 370 whatever its size.
-// Bound by latency: a call takes 4 us before any stream (16 x 512 x 1024), 24 x 4096 x 11008 13.6 us with the quantize,
+// Bound by latency: a call takes 4 us before any stream (16 x 512 x 1024), 24 x 4096 x 11008 13.4 us with the quantize,
 // 45 MB of weights of which are 6.9.  (Up to 64 tokens: 64 x 4096 x 11008 12.8 us here and 19.4 on pairs of SMs, 64 x 9216
 // x 4096 12.1 / 16.3.)
 // -------------------------------------------------------------------------------------------
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(few::THREADS, 2)
     }
     // The token scales may come from the preceding grid, still running when this one starts: no load
     // in front of the wait for it.  They pass through shared memory; read for each column from
-    // global memory they cost 128 round trips in a row (20 us).
+    // global memory they cost a round trip a column in a row.
     grid_wait_prior();
     for (int i = static_cast<int>(threadIdx.x) - 64; i < TOK; i += 256)
       s_tok[i] = i < tokens ? row_scale(args, i) : 0.0f;
@@ -1056,8 +1056,11 @@ static cudaError_t launch_one_m(const OneArgs& o, const GemmInt8Args& a, int fp1
 }
 
 // Columns of a pair tile: the pairs run waves of tiles, and the width that fills its last wave best wins.  A wave takes,
-// in us for a K block of 128, 0.175 with 64 columns to 0.30 with 256 (the last at the MMA's rate, the narrow ones bound by
-// the copies: 53 of 64 bytes a clock into an SM), and the epilogue that nothing overlaps up to 1.6 more than with 64.
+// in us for a K block of 128, 0.175 with 64 columns (bound by the copies: 53 of 64 bytes a clock into an SM) to 0.30 with
+// 256 (bound by the MMA: 0.265 at the full clock, more at the one that the card's power leaves), and the epilogue that
+// nothing overlaps up to 1.6 more than with 64.  The numbers are a fit to whole calls and not a rate for each width: over 51
+// sizes (130 to 8704 tokens, widths 512 to 16384, all six timed in turn) the pick is 0.2 % slower than the best on average
+// and 3 % at most; with 224 columns at 224 / 256 of 0.30, 0.4 % and 7.7 %.
 // Measured on 74 pairs (64 / 128 / 160 / 192 / 224 / 256 columns): 333 x 5120 x 5120 25.7 / 20.0 / 14.5 / 16.2 / 17.1 /
 // 18.6 us, 1500 x 2048 x 8192 37.4 / 28.0 / 29.6 / 21.3 / 22.9 / 25.3, 512 x 4096 x 4096 16.3 / 12.0 / 12.8 / 14.2 / 15.1 / 16.3,
 // 1024 x 9216 x 4096 50.0 / 32.2 / 32.7 / 30.9 / 32.3 / 28.6, 2048 x 12288 x 4096 122 / 80.0 / 72.0 / 71.3 / 69.2 / 78.8.

@@ -159,8 +159,8 @@ cudaError_t launch_rope_table(const void* pos, int pos_is_float, int64_t pos_str
 // E4M3.  So the arithmetic runs on packed pairs of floats, a lane holds sixteen channels (with eight, the address,
 // shuffle and rsqrt work counted twice as much), loads wait in shared memory and not in registers, and bodies without a
 // branch inside are made for 16-bit and E4M3 output, with and without arithmetic: 22 instructions an element became 12.
-// 8704 tokens x 24 heads x 128, Q, K and V: E4M3 43.6 us (5.6 TB/s, 0.86 of the copy bandwidth; 65 % of the issue
-// slots), 4608 tokens bf16 29.8 us (5.8 TB/s, 0.88).
+// 8704 tokens x 24 heads x 128, Q, K and V: E4M3 43.3 us (5.7 TB/s, 0.86 of the copy bandwidth; 65 % of the issue
+// slots), 4608 tokens bf16 29.3 us (5.9 TB/s, 0.90).
 //
 // With adjacent channels as partners (ROT_PAIRS) a packed pair holds the first channels of two partner
 // pairs, another their second channels, so that no half has to be swapped.  With halves as partners and the
