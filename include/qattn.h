@@ -309,7 +309,7 @@ QATTN_API qattn_status qattn_norm_rope(const qattn_norm_rope_io* io, int n_io, i
  *   out[m, k] = rint(127 x[m, k] / amax_m), ties to even, of the exact quotient: -127 .. 127
  * x: device [M, K] bf16 or FP16, ldx elements between rows (any alignment; 16-byte aligned rows are
  * read faster).  out_int8: device [M, K] bytes, ldo between rows, 16-byte aligned, ldo % 16 == 0
- * (what lies between K and ldo is left as it was); it must not overlap x.  scale_dev: device [M].  A row with a
+ * (what lies between K and ldo is left as it was).  scale_dev: device [M].  Neither may overlap x.  A row with a
  * non-finite element gets scale NaN and codes 0 and records QATTN_ERR_NONFINITE; the other rows are
  * not affected. */
 QATTN_API qattn_status qattn_quantize_int8_rows(const void* x, int64_t ldx, qattn_dtype dtype, int M,

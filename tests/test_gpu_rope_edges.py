@@ -7,6 +7,9 @@ product add less than 4 u: 6 u of the value.  The angle: the frequency is held t
 formed by up to 128 products in 64 bits, to 2^-56 of itself, the oracle's FP64 angle to 2^-51: together less than
 |a| 2^-50 + (|pos| + 6) 2^-62.  norm_rope: the bars of test_gpu_rope."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -15,9 +18,10 @@ import torch
 import oracle
 import precision_quantized_attention_b200 as qa
 from precision_quantized_attention_b200 import _lib
-from test_gpu_rope import check_codes
+from test_gpu_rope import _check as check_norm_rope, check_codes
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U = 2.0 ** -24
 # whole numbers near multiples of pi: sines down to 1e-7
 NEAR_PI = [3, 22, 333, 355, 710, 103993, 104348, 208341, 312689, 833719, 1146408]
@@ -167,3 +171,40 @@ def test_running_amax_continues_from_any_number(start):
         qa.norm_rope([qa.NormRopeSegment(x, out, weight=w, amax=amax)])
         assert qa.get_error() == 0
         assert amax.item() == max(np.float32(start), out.abs().max().item())
+
+
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("D", [16, 64, 96, 128, 256])
+def test_a_whole_rotation_next_to_a_norm_without_one(D, inter):
+    """All channels of one tensor rotated, none of another, in one call; each as in a call of its own."""
+    B, L, H = 2, 19, 5
+    g = torch.Generator().manual_seed(D)
+    x = torch.randn(B, L, H, D, generator=g).to(torch.bfloat16).cuda()
+    w = (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    a = torch.rand(L, D // 2, generator=g) * 9
+    table = torch.stack([a.cos(), a.sin()], -1).cuda()
+    forms = [dict(weight=w, table=table), dict(weight=w), dict(table=table), {}]
+    new = lambda: torch.empty(B, H, L, D, dtype=torch.bfloat16, device="cuda")
+    outs = [new() for _ in forms]
+    qa.norm_rope([qa.NormRopeSegment(x, o, **f) for o, f in zip(outs, forms)], interleaved=inter)
+    assert qa.get_error() == 0
+    for o, f in zip(outs, forms):
+        check_norm_rope(o, x, f.get("weight"), f.get("table"), 1e-6, inter, torch.bfloat16)
+    whole = [new(), new()]
+    qa.norm_rope([qa.NormRopeSegment(x, o, **f) for o, f in zip(whole, (forms[0], forms[2]))], interleaved=inter)
+    assert torch.equal(whole[0], outs[0]) and torch.equal(whole[1], outs[2])
+    x[1, 3, 2, D // 2] = float("inf")
+    qa.norm_rope([qa.NormRopeSegment(x, o, **f) for o, f in zip(outs, forms)], interleaved=inter)
+    assert qa.get_error() == _lib.ERR_NONFINITE
+    row = outs[1][1, 2, 3]
+    assert row[D // 2].isnan().item() and int(row.count_nonzero()) == 1      # the others times 1 / infinity
+
+
+@pytest.mark.skipif(_lib.CHECKED, reason="starts the checked-build run")
+def test_edges_pass_in_the_checked_build():
+    from precision_quantized_attention_b200 import build
+    build.build(checked=True)
+    cmd = [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", "tests/test_gpu_rope_edges.py",
+           "tests/test_int8_linear_streams.py", "tests/test_int8_linear_buffers.py"]
+    r = subprocess.run(cmd, cwd=ROOT, env=dict(os.environ, QATTN_DEBUG="1"), capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, (r.stdout + r.stderr)[-4000:]

@@ -95,3 +95,26 @@ def test_a_copied_input_on_a_side_stream(tokens):
     off = abs(want.view(-1, N).double().cpu().numpy() - ref)
     assert (off <= 2.0 ** -8 * abs(ref) + 5 * 2.0 ** -24 * size).all()
     assert qa.get_error() == 0
+
+
+@pytest.mark.gpu
+def test_a_copied_input_on_a_side_stream_of_a_capture():
+    K, N, B, tokens = 256, 96, 3, 9
+    g = torch.Generator().manual_seed(1)
+    whole = torch.randn(B, tokens + 2, K, generator=g).to(torch.bfloat16).cuda()
+    layer = qa.Int8Linear((torch.randn(N, K, generator=g) * K ** -0.5).to(torch.bfloat16).cuda(), max_tokens=64)
+    x = whole[:, :tokens]
+    want = layer(x.contiguous())
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        y = layer(x, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        z = y + 1
+    for scale in (1.0, -3.0):
+        whole.mul_(scale)
+        graph.replay()
+        want = layer(x.contiguous())
+        assert torch.equal(y, want) and torch.equal(z, want + 1)
+    assert qa.get_error() == 0
