@@ -676,7 +676,7 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, unsigned grid, int pairs, in
   bool whole = a.R == a.D;                         // every channel that is computed is rotated
   for (int i = 0; i < a.n; ++i) whole = whole && (a.seg[i].weight == nullptr || a.seg[i].table != nullptr);
   if (pairs && whole) return launch_mode<ROT_PAIRS>(a, grid, fp16 != 0, stream);
-  if (pairs) return launch_mode<ROT_PAIRS_PART>(a, grid, fp16 != 0, stream);
+  if (pairs && a.R > 0) return launch_mode<ROT_PAIRS_PART>(a, grid, fp16 != 0, stream);   // R = 0: ROT_LOW, 1 % faster
   // a whole head rotated by halves: its partner chunks are D / 16 apart, as a lane's two chunks are
   if (whole) return launch_mode<ROT_HALVES>(a, grid, fp16 != 0, stream);
   if (a.R / 8 <= (a.D / 8 + 1) / 2) return launch_mode<ROT_LOW>(a, grid, fp16 != 0, stream);
